@@ -244,6 +244,155 @@ MOE_API moe_status moe_read_error(const moe_cfg* cfg, int32_t T, void* ws, size_
 #define MOE_DEVERR_EXPERT_ID 1   /* routing index outside [0, E) */
 #define MOE_DEVERR_TIMEOUT 2     /* a pipeline wait in a GEMM kernel gave up */
 #define MOE_DEVERR_SCHEDULE 3    /* a GEMM work item was out of range */
+#define MOE_DEVERR_OFFSETS 4     /* row offsets not ascending within [0, R] */
+
+/* ------------------------------------------------------------------------
+ * Training operators of the expert layer.
+ *
+ * moe_layer_forward runs stages 6-8 fused and keeps no intermediate. The calls
+ * below are the same stages as separate operators with their gradients, on
+ * rows grouped by expert (the order moe_permute produces: row r holds slot
+ * perm[r], expert e owns rows offsets[e] .. offsets[e+1]-1), and the optimiser
+ * step of the weights the forward reads:
+ *   G = X Wg_e^T, U = X Wu_e^T        moe_grouped_linear (twice)
+ *   Hw = w * silu(clamp G) clamp U    moe_swiglu
+ *   Y = Hw Wd_e^T                     moe_grouped_linear
+ *   dHw = dY Wd_e, dX = dG Wg_e + dU Wu_e         moe_grouped_linear_dgrad
+ *   dG, dU, dw                                    moe_swiglu_backward
+ *   dWd_e = dY_e^T Hw_e, dWg_e = dG_e^T X_e, ...  moe_grouped_linear_wgrad
+ *   W, m, v                                       moe_adamw_step
+ * The routing weight w multiplies the down product's input, which equals
+ * multiplying its output. The shared expert is the case E = 1, offsets {0, T}.
+ * The conventions at the top of this file hold; sizes are multiples of 8, rows
+ * may be any number from 0 on, and rows at or behind offsets[E] (a receive
+ * buffer's spare rows) are neither used nor written. Outputs overlap no
+ * input unless a call says so. Row-wise tensors of R = 0 rows may be NULL.
+ * --------------------------------------------------------------------- */
+
+#define MOE_T_BF16 0
+#define MOE_T_F32 1
+
+/* Shape of a grouped product. ld_x and ld_y count elements between rows. */
+typedef struct moe_linear_desc {
+  int32_t E;          /* experts, 1 .. 1024 */
+  int32_t R;          /* rows of x and y (capacity), 0 .. 1<<25 */
+  int32_t N;          /* features of y, a multiple of 8, 8 .. 16384 */
+  int32_t K;          /* features of x, a multiple of 8, 8 .. 16384 */
+  int32_t ld_x;       /* row stride of x / dx, >= K, a multiple of 8 */
+  int32_t ld_y;       /* row stride of y / dy, >= N, a multiple of 8 */
+  int32_t out_type;   /* type of the output (y, dx or dW): MOE_T_BF16 or MOE_T_F32 */
+  int32_t accumulate; /* add to the output instead of overwriting it; MOE_T_F32 only (a
+                         running sum held in 16 bits would be rounded at every call) */
+} moe_linear_desc;
+
+/* Bytes of device workspace of the three grouped products (0 on a bad desc).
+ * Its first 256 bytes hold the error word: zero them once, before the first
+ * call. Nothing else is carried from one call to the next. */
+MOE_API size_t moe_linear_workspace_size(const moe_linear_desc* desc);
+
+/* Forward: y[r,:N] (+)= x[r,:K] W_e^T for every row r of every expert e.
+ * x [R, ld_x] bf16, offsets [E+1] int32, W [E,N,K] bf16; out: y [R, ld_y].
+ * fp32 accumulation over K, one rounding at the end. Each call's result is
+ * the same bits every time. Offsets that do not ascend within [0, R] set
+ * MOE_DEVERR_OFFSETS; every access then still stays inside the buffers. */
+MOE_API moe_status moe_grouped_linear(const moe_linear_desc* desc, const void* x,
+                                      const int32_t* offsets, const void* W, void* y, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* Gradient of the input: dx[r,:K] (+)= dy[r,:N] W_e. dy [R, ld_y] bf16,
+ * W [E,N,K] bf16; out: dx [R, ld_x]. Otherwise as moe_grouped_linear. */
+MOE_API moe_status moe_grouped_linear_dgrad(const moe_linear_desc* desc, const void* dy,
+                                            const int32_t* offsets, const void* W, void* dx,
+                                            void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the weights: dW[e] (+)= sum over the rows r of e of
+ * dy[r,:N]^T x[r,:K]. dy [R, ld_y] and x [R, ld_x] bf16; out: dW [E,N,K],
+ * zeros for an expert without rows (untouched when accumulating). What stands
+ * in rows that belong to no expert, NaN included, has no effect. */
+MOE_API moe_status moe_grouped_linear_wgrad(const moe_linear_desc* desc, const void* dy,
+                                            const void* x, const int32_t* offsets, void* dW,
+                                            void* ws, size_t ws_bytes, void* stream);
+
+/* moe_read_error for the workspace of the grouped products. */
+MOE_API moe_status moe_linear_read_error(void* ws, size_t ws_bytes, void* stream, int32_t* code);
+
+/* Rows of SwiGLU. ld_*: elements between rows, >= I, multiples of 8. */
+typedef struct moe_swiglu_desc {
+  int32_t R;      /* rows (capacity), 0 .. 1<<25 */
+  int32_t I;      /* features, a multiple of 8, 8 .. 16384 */
+  int32_t ld_g;   /* of g and u (a gate | up buffer of 2I columns has ld_g = 2I) */
+  int32_t ld_h;   /* of h and dh */
+  int32_t ld_dg;  /* of dg and du (backward only) */
+  float limit;    /* clamp g and u to [-limit, limit] first; <= 0 or inf: off */
+} moe_swiglu_desc;
+
+/* h[r,i] = bf16(w * silu(clamp(g[r,i])) * clamp(u[r,i])).
+ * g, u [R, ld_g] and h [R, ld_h] bf16. w fp32, nullable (1): the weight of row
+ * r is w[perm[r]], or w[r] where perm (int32 [R]) is NULL. rows: device int32,
+ * nullable (R), 4-byte aligned (offsets + E will do): rows at or behind
+ * *rows are left as they are. With perm, w has
+ * n_w entries (ignored otherwise); a row whose perm entry lies outside
+ * [0, n_w) gets NaN. NaN in g or u stays NaN. h may be g or u (same stride). */
+MOE_API moe_status moe_swiglu(const moe_swiglu_desc* desc, const void* g, const void* u,
+                              const float* w, const int32_t* perm, int32_t n_w,
+                              const int32_t* rows, void* h, void* stream);
+
+/* Gradients of moe_swiglu for dh, the gradient of h:
+ *   dg = w dh clamp(u) s (1 + a (1 - s)), s = sigmoid(a), a = clamp(g), where
+ *        |g| <= limit, else 0;  du = w dh silu(a) where |u| <= limit, else 0;
+ *   dw[perm[r]] = sum_i dh[r,i] silu(a) clamp(u)   (fp32; needs w; nullable).
+ * dg, du [R, ld_dg] bf16 (they may be g and u). dw entries of no row are left
+ * as they are; rows that name the same entry (perm is no permutation) are
+ * refused by no check and leave one of their sums. */
+MOE_API moe_status moe_swiglu_backward(const moe_swiglu_desc* desc, const void* dh, const void* g,
+                                       const void* u, const float* w, const int32_t* perm,
+                                       int32_t n_w, const int32_t* rows, void* dg, void* du,
+                                       float* dw, void* stream);
+
+/* One tensor of an AdamW step. All pointers device; the scales 4-byte aligned,
+ * everything else 16-byte. */
+#define MOE_STATE_F32 0 /* m and v fp32 [n] */
+#define MOE_STATE_8BIT 1
+/* 8-bit states: m and v are e4m3 codes [n] with one fp32 scale per block of
+ * MOE_STATE_BLOCK elements counted from the tensor's start (ceil(n / block)
+ * scales, the last block may be short): m = code * m_scale, and sqrt(v) (not
+ * v, whose range would not fit) = code * v_scale. scale = max|.| / 448 over
+ * the block, 0 when the maximum is below 2^-100 (the block is then zero).
+ * Codes round to nearest even; a nonzero sqrt(v) is never rounded to zero (it
+ * divides the update) but up to the smallest code, 2^-9. */
+#define MOE_STATE_BLOCK 256
+typedef struct moe_adamw_tensor {
+  void* p;             /* parameters [n], p_type; updated */
+  float* master;       /* fp32 parameters [n], nullable: p then is their rounding */
+  const void* g;       /* gradient [n], g_type */
+  void* m;             /* first moment, updated */
+  void* v;             /* second moment, updated */
+  float* m_scale;      /* MOE_STATE_8BIT only, updated */
+  float* v_scale;
+  int64_t n;           /* elements, 0 allowed */
+  int32_t p_type;      /* MOE_T_BF16 or MOE_T_F32 (F32: master must be NULL) */
+  int32_t g_type;      /* MOE_T_BF16 or MOE_T_F32 */
+  int32_t state_type;  /* MOE_STATE_F32 or MOE_STATE_8BIT */
+  float wd_scale;      /* times weight_decay for this tensor (0: no decay) */
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_cfg {
+  double lr, beta1, beta2, eps, weight_decay;
+  double grad_scale;   /* multiplies every gradient (1, or a clipping factor) */
+  int64_t step;        /* 1 for the first step */
+  const float* dyn;    /* nullable device [4]: lr, 1 - beta1^step, sqrt(1 - beta2^step) and
+                          grad_scale, read when the step runs in place of the fields above, so
+                          that a captured graph can follow a schedule */
+} moe_adamw_cfg;
+
+/* One AdamW step over n_tensors tensors (host array, read during the call):
+ *   g' = grad_scale g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, p taken from master where there is one. The update uses m and v
+ * before they are rounded to 8 bits. A non-finite gradient makes its element
+ * non-finite, with 8-bit states its block. Tensors must not overlap. */
+MOE_API moe_status moe_adamw_step(const moe_adamw_cfg* cfg, const moe_adamw_tensor* tensors,
+                                  int32_t n_tensors, void* stream);
 
 /* Human-readable name of a status. Never NULL. */
 MOE_API const char* moe_status_string(moe_status s);

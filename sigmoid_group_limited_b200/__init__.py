@@ -2,7 +2,8 @@
 
 Argument marshalling only: every stage runs in the library's CUDA kernels.
 The names mirror the C-ABI in include/moe.h (moe_route, moe_permute,
-moe_grouped_swiglu, moe_combine, moe_layer_forward). Tensors are torch CUDA
+moe_grouped_swiglu, moe_combine, moe_layer_forward; the training operators
+are in training.py and exported here). Tensors are torch CUDA
 tensors (torch provides device memory and streams); bf16 tensors may be
 torch.bfloat16 or int16/uint16 views of the same bytes.
 
@@ -29,12 +30,14 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_CFG", -2: "MOE_ERR_NULL", -3: "MOE_ERR_ALIGN
           -4: "MOE_ERR_WORKSPACE", -5: "MOE_ERR_CUDA", -6: "MOE_ERR_DEVICE",
           -7: "MOE_ERR_UNSUPPORTED"}
 DEVERR = {0: "none", 1: "expert id out of range", 2: "pipeline wait timed out",
-          3: "work item out of range"}
+          3: "work item out of range", 4: "row offsets not ascending within the rows"}
 
 C_FUNCTIONS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_permute_static", "moe_route_stats",
                "moe_grouped_swiglu", "moe_prepare_weights",
                "moe_combine", "moe_layer_forward", "moe_read_error", "moe_status_string",
-               "moe_version")
+               "moe_version", "moe_linear_workspace_size", "moe_grouped_linear",
+               "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad", "moe_linear_read_error",
+               "moe_swiglu", "moe_swiglu_backward", "moe_adamw_step")
 
 
 class MoEError(RuntimeError):
@@ -89,6 +92,7 @@ def lib() -> ctypes.CDLL:
               "moe_combine", "moe_prepare_weights",
               "moe_layer_forward", "moe_read_error"):
         getattr(L, f).restype = i32
+    training.declare(L)
     _lib = L
     return L
 
@@ -220,3 +224,13 @@ def moe_read_error(cfg, T, ws, stream=None) -> int:
 
 def version() -> str:
     return lib().moe_version().decode()
+
+
+from . import training  # noqa: E402  (needs the names above)
+from .training import (  # noqa: E402,F401
+    MOE_STATE_8BIT, MOE_STATE_BLOCK, MOE_STATE_F32, MOE_T_BF16, MOE_T_F32, adamw_dyn,
+    alloc_linear_workspace, linear_workspace_size, make_adamw_tensors, moe_adamw_cfg,
+    moe_adamw_step, moe_adamw_tensor, moe_grouped_linear, moe_grouped_linear_dgrad,
+    moe_grouped_linear_wgrad, moe_linear_desc, moe_linear_read_error, moe_swiglu,
+    moe_swiglu_backward, moe_swiglu_desc)
+

@@ -1,0 +1,176 @@
+// act.cu - SwiGLU with its limit and routing weight, forward and backward
+// (moe_swiglu, moe_swiglu_backward).
+//
+//   a = clamp(g), b = clamp(u), s = 1 / (1 + e^-a)
+//   h  = w a s b
+//   dg = w dh b (s + a s (1 - s)) where |g| <= limit, else 0
+//   du = w dh a s                 where |u| <= limit, else 0
+//   dw = sum_i dh a s b
+//
+// Both are bound by HBM: 6 bytes per element forward (g, u in, h out), 10
+// backward. A group of G lanes owns a row (so dw is one shuffle reduction,
+// in a fixed order) and moves 8 features (16 bytes) per lane and tensor.
+// Everything between the loads and the one rounding of each output is fp32;
+// the exponential is the hardware one (a few ulp, far below bf16's half ulp).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+
+namespace sgl {
+namespace {
+
+constexpr int kActThreads = 256;
+
+struct ActParams {
+  int R, chunks;  // rows, 8-feature pieces per row
+  long long ld_g, ld_h, ld_dg;
+  float limit;  // inf: off
+  const uint16_t *dh, *g, *u;
+  const float* w;
+  const int32_t* perm;
+  int n_w;
+  const int32_t* rows;
+  uint16_t *h, *dg, *du;
+  float* dw;
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ uint4 load8(const uint16_t* p, long long at) {
+  return __ldcs(reinterpret_cast<const uint4*>(p + at));
+}
+__device__ __forceinline__ void store8(uint16_t* p, long long at, const uint4& v) {
+  *reinterpret_cast<uint4*>(p + at) = v;
+}
+// The limit as comparisons, which keep a NaN (fminf / fmaxf would drop it).
+__device__ __forceinline__ float clamp_nan(float v, float L) {
+  return v > L ? L : (v < -L ? -L : v);
+}
+__device__ __forceinline__ float sigmoid_fast(float a) {
+  return __fdividef(1.f, 1.f + __expf(-a));
+}
+
+// Routing weight of row r and where its gradient goes (-1: nowhere).
+__device__ __forceinline__ float row_weight(const ActParams& p, int r, long long* slot) {
+  *slot = -1;
+  if (p.w == nullptr) return 1.f;
+  long long j = r;
+  if (p.perm != nullptr) {
+    j = p.perm[r];
+    if (j < 0 || j >= p.n_w) return __int_as_float(0x7fc00000);
+  }
+  *slot = j;
+  return p.w[j];
+}
+
+template <int G, bool BWD>
+__global__ void __launch_bounds__(kActThreads) act_kernel(const ActParams p) {
+  const int live = p.rows ? max(0, min(*p.rows, p.R)) : p.R;
+  const int lane = threadIdx.x % G;
+  const int per = kActThreads / G;
+  for (int r = blockIdx.x * per + threadIdx.x / G; r < live; r += gridDim.x * per) {
+    long long slot;
+    const float w = row_weight(p, r, &slot);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < p.chunks; c += G) {
+      float g[8], u[8], dh[8], o[8], o2[8];
+      unpack8(load8(p.g, r * p.ld_g + 8 * c), g);
+      unpack8(load8(p.u, r * p.ld_g + 8 * c), u);
+      if (BWD) unpack8(load8(p.dh, r * p.ld_h + 8 * c), dh);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = clamp_nan(g[i], p.limit), b = clamp_nan(u[i], p.limit);
+        const float s = sigmoid_fast(a);
+        const float silu = a * s;
+        if (!BWD) {
+          o[i] = w * silu * b;
+        } else {
+          sum += dh[i] * (silu * b);
+          const float wd = w * dh[i];
+          o[i] = fabsf(g[i]) > p.limit ? 0.f : wd * b * (s + silu * (1.f - s));
+          o2[i] = fabsf(u[i]) > p.limit ? 0.f : wd * silu;
+        }
+      }
+      if (!BWD) {
+        store8(p.h, r * p.ld_h + 8 * c, pack8(o));
+      } else {
+        store8(p.dg, r * p.ld_dg + 8 * c, pack8(o));
+        store8(p.du, r * p.ld_dg + 8 * c, pack8(o2));
+      }
+    }
+    if (BWD && p.dw != nullptr) {
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(__activemask(), sum, o, G);
+      if (lane == 0 && slot >= 0) p.dw[slot] = sum;
+    }
+  }
+}
+
+template <bool BWD>
+cudaError_t launch_act(const ActParams& p, cudaStream_t s) {
+  const int per = kActThreads / 32;
+  const int grid = min(cdiv(p.R, per), num_sms() * 8);
+  act_kernel<32, BWD><<<grid, kActThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+ActParams common(const moe_swiglu_desc& d, const void* g, const void* u, const float* w,
+                 const int32_t* perm, int n_w, const int32_t* rows) {
+  ActParams p = {};
+  p.R = d.R;
+  p.chunks = d.I / 8;
+  p.ld_g = d.ld_g;
+  p.ld_h = d.ld_h;
+  p.ld_dg = d.ld_dg;
+  p.limit = d.limit > 0.f ? d.limit : INFINITY;
+  p.g = static_cast<const uint16_t*>(g);
+  p.u = static_cast<const uint16_t*>(u);
+  p.w = w;
+  p.perm = perm;
+  p.n_w = n_w;
+  p.rows = rows;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu(const moe_swiglu_desc& d, const void* g, const void* u, const float* w,
+                          const int32_t* perm, int n_w, const int32_t* rows, void* h,
+                          cudaStream_t s) {
+  ActParams p = common(d, g, u, w, perm, n_w, rows);
+  p.h = static_cast<uint16_t*>(h);
+  return launch_act<false>(p, s);
+}
+
+cudaError_t launch_swiglu_backward(const moe_swiglu_desc& d, const void* dh, const void* g,
+                                   const void* u, const float* w, const int32_t* perm, int n_w,
+                                   const int32_t* rows, void* dg, void* du, float* dw,
+                                   cudaStream_t s) {
+  ActParams p = common(d, g, u, w, perm, n_w, rows);
+  p.dh = static_cast<const uint16_t*>(dh);
+  p.dg = static_cast<uint16_t*>(dg);
+  p.du = static_cast<uint16_t*>(du);
+  p.dw = dw;
+  return launch_act<true>(p, s);
+}
+
+}  // namespace sgl

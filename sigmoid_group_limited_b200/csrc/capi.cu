@@ -40,6 +40,21 @@ cudaError_t ensure_dyn_smem(const void* func, int bytes) {
   return e;
 }
 
+// sm_100 check, cached per device.
+moe_status device_ok() {
+  static int cache[64] = {0};  // 0 unknown, 1 ok, 2 not ok
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
+  if (cache[dev] == 0) {
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    cache[dev] = (major == 10 && minor == 0) ? 1 : 2;
+  }
+  return cache[dev] == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 WsLayout ws_layout(const moe_cfg& c, int T) {
@@ -146,21 +161,6 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool fused_front_disabled() {
   const char* v = getenv("SGL_MOE_FRONT");
   return v != nullptr && strcmp(v, "separate") == 0;
-}
-
-// sm_100 check, cached per device.
-moe_status device_ok() {
-  static int cache[64] = {0};  // 0 unknown, 1 ok, 2 not ok
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-  if (dev < 0 || dev >= 64) return MOE_ERR_UNSUPPORTED;
-  if (cache[dev] == 0) {
-    int major = 0, minor = 0;
-    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-    cache[dev] = (major == 10 && minor == 0) ? 1 : 2;
-  }
-  return cache[dev] == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 template <typename T>

@@ -283,6 +283,24 @@ cudaError_t launch_route_stats(const moe_cfg& c, const int32_t* counts, double* 
 
 int num_sms();
 
+// MOE_OK on an sm_100 device, MOE_ERR_UNSUPPORTED elsewhere; cached per device.
+moe_status device_ok();
+
+// Training operators (validated by the entry points in capi_train.cu).
+// The direction of a grouped product.
+enum LinearDir { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const void* a,
+                                  const void* b, const int32_t* offsets, void* out, int32_t* err,
+                                  cudaStream_t s);
+cudaError_t launch_swiglu(const moe_swiglu_desc& d, const void* g, const void* u, const float* w,
+                          const int32_t* perm, int n_w, const int32_t* rows, void* h,
+                          cudaStream_t s);
+cudaError_t launch_swiglu_backward(const moe_swiglu_desc& d, const void* dh, const void* g,
+                                   const void* u, const float* w, const int32_t* perm, int n_w,
+                                   const int32_t* rows, void* dg, void* du, float* dw,
+                                   cudaStream_t s);
+cudaError_t launch_adamw(const moe_adamw_cfg& c, const moe_adamw_tensor* t, int n, cudaStream_t s);
+
 // Tensor map of a bf16 row-major [rows, cols] matrix for TMA: box of
 // box_rows x 64 columns, 128-byte swizzle. False if it cannot be encoded.
 bool map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
