@@ -304,6 +304,13 @@ cudaError_t launch_adamw(const moe_adamw_cfg& c, const moe_adamw_tensor* t, int 
 // Tensor map of a bf16 row-major [rows, cols] matrix for TMA: box of
 // box_rows x 64 columns, 128-byte swizzle. False if it cannot be encoded.
 bool map_bf16(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// The same with rows `ld` elements apart, and [blocks, rows, cols] matrices one
+// after another (coordinates column, row, block): what lies past a row's or a
+// block's end reads as zero. ld and cols are multiples of 8.
+bool map_bf16_ld(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
+                 uint32_t box_rows);
+bool map_bf16_blocks(CUtensorMap* m, const void* ptr, uint64_t blocks, uint64_t rows,
+                     uint64_t cols, uint32_t box_rows);
 // Row-major [rows, cols] bytes (e4m3 codes): box of box_rows x 128 bytes,
 // 128-byte swizzle.
 bool map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);

@@ -1,110 +1,516 @@
 // linear.cu - products grouped by expert with ragged row counts
-// (moe_grouped_linear and its two gradients).
+// (moe_grouped_linear and its two gradients) on CTA pairs (tcgen05
+// cta_group::2).
 //
 //   forward  y[r,n]    = sum_k x[r,k]  W[e,n,k]      rows r of expert e
 //   dgrad    dx[r,k]   = sum_n dy[r,n] W[e,n,k]
 //   wgrad    dW[e,n,k] = sum_r dy[r,n] x[r,k]
 //
-// The simple form: 64 x 64 output tiles, fp32 fused multiply-adds.
+// One kernel, three sets of operands. A pair of CTAs (a cluster of two) owns
+// an output tile D[256][up to 256]: M = 256 MMAs, each CTA with 128 rows of A
+// and half of B's columns in its shared memory and 128 rows of D in its
+// tensor memory. Forward and dgrad put the features (regular, hundreds) on M
+// and an expert's rows (ragged) on N, so a short tile costs a narrower MMA,
+// not a padded one; wgrad has features on both sides and the ragged rows as
+// the contraction.
+//
+//   direction  M (A)                N (B)               contraction
+//   forward    n: W, K-major        rows: x, K-major    k
+//   dgrad      k: W, MN-major       rows: dy, K-major   n
+//   wgrad      n: dy, MN-major      k: x, MN-major      rows
+//
+// MN-major operands are read in place: the TMA box is 64 features wide and 64
+// contraction indices high, and the MMA transposes. The tensor maps end at
+// the tensors' ends, so features past N or K read as zeros. Rows are another
+// matter: behind an expert's rows come the next one's. On N they only fill
+// columns that are never stored. In wgrad's contraction they must not count,
+// whatever they hold: the last block runs only the 16-row steps that have
+// rows, and a warp of each CTA zeroes the rest of the last step in shared
+// memory (NaN times zero would be NaN) before the MMA may read the stage.
+//
+// Persistent: pair i takes tiles i, i + pairs, ...; every role finds its
+// tiles from the row offsets by itself, so there is no queue, no counter and
+// no state between calls, and the same call always adds in the same order.
+// Two 256-column accumulators: a tile's epilogue runs under the next tile's
+// MMAs.
+//
+// Warp roles per CTA (384 threads):
+//   0      TMA producer (lane 0)
+//   1      TMEM allocation; MMA issuer (lane 0) in the leader
+//   2      wgrad: zeroes the rows behind an expert's last
+//   3      idle
+//   4..11  epilogue, two warps per TMEM lane quarter, alternate column chunks
+// Every wait is bounded and raises the error word.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
+#include "ffn_common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace sgl {
 namespace {
 
-constexpr int kTile = 64, kDeep = 16, kThreads = 256;
+constexpr int kLinThreads = 384;
+constexpr int kLinEpiWarp0 = 4, kLinEpiWarps = 8;
+constexpr int kLinStages = 6;
+constexpr int kLinHalf = 128 * 128;         // one operand's stage: 128 rows of 128 bytes
+constexpr int kLinStage = 2 * kLinHalf;     // A, B
+constexpr int kLinTile = 256;               // features on M, columns on N
+constexpr int kLinEpi = 32 * 80;            // a warp's transposition tile
+constexpr int kLinCtrl = 512;
+constexpr int kLinSmem = kLinStages * kLinStage + kLinEpiWarps * kLinEpi + kLinCtrl + 1024;
+static_assert(kLinSmem + (2 * kMaxExpertsCfg + 3 + 33) * 4 <= 227 * 1024, "shared memory");
 
 struct LinParams {
-  int E, R, N, K;
-  long long ld_x, ld_y;
+  int E, R;
+  int M, C;        // features on M; on N (wgrad only)
+  int depth;       // contraction length (forward, dgrad)
+  int mt, ct;      // feature tiles on M; on N (wgrad only)
+  long long ld;    // output row stride
   int out_f32, accumulate;
-  const uint16_t *a, *b;
   const int32_t* offsets;
   void* out;
   int32_t* err;
 };
 
-__device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+struct LinMaps {
+  CUtensorMap a;       // forward: W, 128-row boxes; dgrad: W, wgrad: dy, 64-row boxes
+  CUtensorMap b, b32;  // forward, dgrad: rows, boxes of 128 and of 32; wgrad: x, 64-row boxes
+};
 
-// Rows [lo, hi) of expert e, held inside [0, R] whatever the offsets say.
-__device__ __forceinline__ int2 expert_range(const LinParams& p, int e) {
-  const int a = p.offsets[e], b = p.offsets[e + 1];
-  if (a < 0 || b < a || b > p.R) atomicExch(p.err, MOE_DEVERR_OFFSETS);
-  const int lo = min(max(a, 0), p.R);
-  return make_int2(lo, min(max(b, lo), p.R));
+struct LinTile {
+  int e, m0, c0;   // expert, first feature on M, first column (token row / feature)
+  int rows, cols;  // rows of the contraction (wgrad) or of the tile; columns to store
+  int n;           // MMA N: cols rounded up to 32
+};
+
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  const __nv_bfloat16 b = __float2bfloat16(v);
+  return *reinterpret_cast<const uint16_t*>(&b);
+}
+
+// A warp's 32-row tile in shared memory (rows of 64 payload bytes, 80 apart)
+// to global memory: lane l moves 16 bytes of rows l / 4 + 8 i. `at(row)` is the
+// address of a row's first byte or null, `left` the payload bytes that exist.
+template <bool ADD, typename At>
+__device__ __forceinline__ void store_rows64(const uint8_t* tile, int lane, int left, At at) {
+  const int piece = (lane & 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = lane / 4 + 8 * i;
+    uint8_t* g = at(r);
+    if (g != nullptr && piece < left) {
+      float4 v = *reinterpret_cast<const float4*>(tile + r * 80 + piece);
+      float4* o = reinterpret_cast<float4*>(g + piece);
+      if (ADD) {
+        const float4 w = *o;
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      *o = v;
+    }
+  }
 }
 
 template <int DIR>
-__global__ void __launch_bounds__(kThreads) linear_simple(const LinParams p) {
-  __shared__ float sa[kDeep][kTile + 1], sb[kDeep][kTile + 1];
-  const int cols = DIR == kFwd ? p.N : p.K;
-  const int c0 = blockIdx.y * kTile;
-  int e = blockIdx.z, lo = 0, hi = 0, m0 = 0, m_end = 0;
-  if (DIR == kWgrad) {
-    const int2 r = expert_range(p, e);
-    lo = r.x, hi = r.y;
-    m0 = blockIdx.x * kTile, m_end = p.N;
-  } else {  // blockIdx.x: a 64-row tile, counted over the experts
-    int left = blockIdx.x;
-    for (e = 0; e < p.E; ++e) {
-      const int2 r = expert_range(p, e);
-      const int tiles = (r.y - r.x + kTile - 1) / kTile;
-      if (left < tiles) {
-        m0 = r.x + left * kTile, m_end = r.y;
-        break;
-      }
-      left -= tiles;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+    grouped_linear(const __grid_constant__ LinParams p, const __grid_constant__ LinMaps m) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* epi = smem + kLinStages * kLinStage;
+  uint8_t* ctrl = epi + kLinEpiWarps * kLinEpi;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [stages] (the leader's count)
+  uint64_t* empty = full + kLinStages;                 // [stages]
+  uint64_t* tail = empty + kLinStages;                 // [stages] wgrad: a last block has landed
+  uint64_t* tfull = tail + kLinStages;                 // [2]
+  uint64_t* tempty = tfull + 2;                        // [2] (the leader's count)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* bad = const_cast<int*>(abort_flag) + 1;
+  static_assert(8 * (3 * kLinStages + 4) + 12 <= kLinCtrl, "ctrl");
+  int* s_off = reinterpret_cast<int*>(ctrl + kLinCtrl);  // [E+1] row offsets
+  int* s_tile = s_off + p.E + 1;                         // [E+1] tiles before expert e
+  int* wsum = s_tile + p.E + 1;                          // [33]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank() & 1u;
+  const bool leader = rank == 0;
+  if (tid == 0) {
+    for (int s = 0; s < kLinStages; ++s) {
+      // the leader's producer; wgrad: two arrivals, its producer's or, for a
+      // last block, one of each CTA's zeroing warp
+      mbar_init(&full[s], DIR == kWgrad ? 2 : 1);
+      mbar_init(&empty[s], 1);  // the leader's multicast commit
+      mbar_init(&tail[s], 1);
     }
-    if (e == p.E) return;
-    hi = DIR == kFwd ? p.K : p.N;
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);                  // multicast commit
+      mbar_init(&tempty[a], 2 * kLinEpiWarps);  // the epilogue warps of both CTAs
+    }
+    *abort_flag = 0;
+    *bad = 0;
+    fence_mbar_init();
+    if (p.R > 0) {
+      prefetch_tmap(&m.a);
+      prefetch_tmap(&m.b);
+    }
   }
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int k0 = lo; k0 < hi; k0 += kDeep) {
-    for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-      const int t = i % kTile, d = k0 + i / kTile;
-      float av = 0.f, bv = 0.f;
-      if (d < hi) {
-        if (m0 + t < m_end)
-          av = DIR == kWgrad ? bf(p.a[d * p.ld_y + m0 + t])
-                             : bf(p.a[(m0 + t) * (DIR == kFwd ? p.ld_x : p.ld_y) + d]);
-        if (c0 + t < cols)
-          bv = DIR == kWgrad ? bf(p.b[d * p.ld_x + c0 + t])
-               : DIR == kFwd ? bf(p.b[(static_cast<long long>(e) * p.N + c0 + t) * p.K + d])
-                             : bf(p.b[(static_cast<long long>(e) * p.N + d) * p.K + c0 + t]);
-      }
-      sa[i / kTile][t] = av;
-      sb[i / kTile][t] = bv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[d][ty * 4 + i] * sb[d][tx * 4 + j];
-    __syncthreads();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
-  if (DIR == kWgrad && lo == hi && p.accumulate) return;
-  const long long ld = DIR == kFwd ? p.ld_y : DIR == kDgrad ? p.ld_x : p.K;
-  const long long row0 = DIR == kWgrad ? static_cast<long long>(e) * p.N : 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, c = c0 + tx * 4 + j;
-      if (m >= m_end || c >= cols) continue;
-      const long long at = (row0 + m) * ld + c;
-      if (p.out_f32) {
-        float* o = static_cast<float*>(p.out) + at;
-        *o = p.accumulate ? *o + acc[i][j] : acc[i][j];
-      } else {
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(acc[i][j]);
+  for (int i = tid; i <= p.E; i += kLinThreads) s_off[i] = p.offsets[i];
+  tc_fence_before();
+  __syncthreads();
+  for (int e = tid; e <= p.E; e += kLinThreads) {
+    const int lo = s_off[e], hi = e < p.E ? s_off[e + 1] : p.R;
+    if (lo < 0 || hi < lo || hi > p.R) *bad = 1;
+    s_tile[e] = e == p.E ? 0
+                : DIR == kWgrad ? p.mt * p.ct
+                                : p.mt * ((hi - lo + kLinTile - 1) / kLinTile);
+  }
+  __syncthreads();
+  const bool go = *bad == 0;  // the same in every CTA: all read the same offsets
+  if (!go && tid == 0) atomicExch(p.err, MOE_DEVERR_OFFSETS);
+  if (go) smem_exscan(s_tile, p.E + 1, wsum);
+  cluster_sync();  // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int tiles = go ? s_tile[p.E] : 0;
+  const int first = blockIdx.x / 2, pairs = gridDim.x / 2;
+  auto at_leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
+
+  // Tile i; e: the expert of the caller's previous tile (tiles ascend).
+  auto tile_at = [&](int i, int e) {
+    LinTile t;
+    while (s_tile[e + 1] <= i) ++e;
+    const int local = i - s_tile[e];
+    const int rows = s_off[e + 1] - s_off[e];
+    t.e = e;
+    t.m0 = (local % p.mt) * kLinTile;
+    const int c = (local / p.mt) * kLinTile;
+    if (DIR == kWgrad) {
+      t.c0 = c;
+      t.rows = rows;
+      t.cols = min(kLinTile, p.C - c);
+    } else {
+      t.c0 = s_off[e] + c;
+      t.cols = t.rows = min(kLinTile, rows - c);
+    }
+    t.n = (t.cols + 31) & ~31;
+    return t;
+  };
+  auto depth_of = [&](const LinTile& t) { return DIR == kWgrad ? t.rows : p.depth; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last(), pol_w = policy_evict_first();
+      int stage = 0, e = 0;
+      uint32_t phase = 0;
+      bool live = true;
+      for (int i = first; i < tiles && live; i += pairs) {
+        const LinTile t = tile_at(i, e);
+        e = t.e;
+        const int depth = depth_of(t), half = t.n / 2;
+        const int am = t.m0 + static_cast<int>(rank) * 128;
+        const int bc = t.c0 + static_cast<int>(rank) * half;
+        // boxes of B: 32 or 128 rows high (forward, dgrad), 64 features wide (wgrad)
+        const int bbox = DIR == kWgrad ? 64 : half == 128 ? 128 : 32;
+        const int nbox = (half + bbox - 1) / bbox;
+        const uint32_t bytes = kLinHalf + nbox * bbox * 128;
+        // weights that one tile column reads are not needed again
+        const uint64_t pa = DIR != kWgrad && s_off[t.e + 1] - s_off[t.e] <= kLinTile ? pol_w : pol;
+        for (int k0 = 0; k0 < depth; k0 += 64) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+            live = false;
+            break;
+          }
+          uint8_t* sA = smem + stage * kLinStage;
+          uint8_t* sB = sA + kLinHalf;
+          if (DIR == kWgrad) {
+            const int row = s_off[t.e] + k0;
+            const int rest = depth - k0;
+            if (rest < 64 && rest % 16 != 0) {  // zeroed before it counts as full
+              mbar_arrive_expect_tx(&tail[stage], bytes);
+              for (int h = 0; h < 2; ++h)
+                tma_load_2d(sA + h * 8192, &m.a, &tail[stage], am + 64 * h, row, pol);
+              for (int h = 0; h < nbox; ++h)
+                tma_load_2d(sB + h * 8192, &m.b, &tail[stage], bc + 64 * h, row, pol);
+            } else {
+              const uint32_t bar = at_leader(&full[stage]);
+              if (leader) {
+                mbar_arrive(&full[stage]);
+                mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+              }
+              for (int h = 0; h < 2; ++h)
+                tma_load_2d_pair(sA + h * 8192, &m.a, bar, am + 64 * h, row, pol);
+              for (int h = 0; h < nbox; ++h)
+                tma_load_2d_pair(sB + h * 8192, &m.b, bar, bc + 64 * h, row, pol);
+            }
+          } else {
+            const uint32_t bar = at_leader(&full[stage]);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            if (DIR == kFwd) {
+              tma_load_3d_pair(sA, &m.a, bar, k0, am, t.e, pa);
+            } else {
+              for (int h = 0; h < 2; ++h)
+                tma_load_3d_pair(sA + h * 8192, &m.a, bar, am + 64 * h, k0, t.e, pa);
+            }
+            for (int h = 0; h < nbox; ++h)
+              tma_load_2d_pair(sB + h * bbox * 128, bbox == 128 ? &m.b : &m.b32, bar, k0,
+                               bc + h * bbox, pol);
+          }
+          if (++stage == kLinStages) stage = 0, phase ^= 1;
+        }
+      }
+      // every stage must be released by the MMA before teardown
+      for (int i = 0; i < kLinStages && live; ++i) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
+        if (++stage == kLinStages) stage = 0, phase ^= 1;
+      }
+      // after a timeout: time for the copies and MMAs in flight to end (they take microseconds)
+      if (*abort_flag)
+        for (const long long t0 = clock64(); clock64() - t0 < 4000000;) {}
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      constexpr uint32_t major = DIR == kFwd ? 0 : DIR == kDgrad ? kIdescMnA : kIdescMnA | kIdescMnB;
+      int stage = 0, e = 0;
+      uint32_t phase = 0, used = 0;  // used: accumulators taken so far
+      bool live = true;
+      for (int i = first; i < tiles && live; i += pairs) {
+        const LinTile t = tile_at(i, e);
+        e = t.e;
+        const int depth = depth_of(t);
+        if (depth == 0) continue;
+        const uint32_t buf = used & 1, idesc = idesc_bf16(2 * 128, t.n) | major;
+        if (!mbar_wait_cluster(&tempty[buf], ((used >> 1) & 1) ^ 1, abort_flag, p.err,
+                               MOE_DEVERR_TIMEOUT))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * kLinTile;
+        for (int k0 = 0; k0 < depth; k0 += 64) {
+          if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+            live = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + stage * kLinStage), b0 = a0 + kLinHalf;
+          const int steps = min(4, (depth - k0 + 15) / 16);
+          for (int k = 0; k < steps; ++k) {
+            const uint64_t da = DIR == kFwd ? sdesc_k128(a0 + k * 32) : sdesc_mn128(a0 + k * 2048, 8192);
+            const uint64_t db = DIR == kWgrad ? sdesc_mn128(b0 + k * 2048, 8192) : sdesc_k128(b0 + k * 32);
+            umma_bf16_pair(d, da, db, idesc, (k0 | k) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both CTAs
+          if (++stage == kLinStages) stage = 0, phase ^= 1;
+        }
+        if (!live) break;
+        umma_commit_pair_mc(&tfull[buf], 0x3);
+        ++used;
       }
     }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ zeroing of ragged ends (wgrad)
+    if (DIR == kWgrad) {
+      int stage = 0, e = 0;
+      uint32_t seen = 0;  // bit s: parity of stage s's tail barrier
+      bool live = true;
+      for (int i = first; i < tiles && live; i += pairs) {
+        const LinTile t = tile_at(i, e);
+        e = t.e;
+        const int blocks = (t.rows + 63) / 64, rest = t.rows % 64;
+        if (rest % 16 != 0) {
+          const int s = (stage + blocks - 1) % kLinStages;
+          if (!mbar_wait(&tail[s], (seen >> s) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
+          seen ^= 1u << s;
+          // whole 128-byte rows: the swizzle moves pieces inside a row only
+          uint8_t* base = smem + s * kLinStage;
+          const int nrow = 16 - rest % 16;
+          for (int j = lane; j < 4 * nrow * 8; j += 32) {
+            const int box = j / (nrow * 8), row = rest + (j / 8) % nrow;
+            *reinterpret_cast<uint4*>(base + box * 8192 + row * 128 + (j % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) mbar_arrive(&full[s]);
+            else mbar_arrive_cluster(at_leader(&full[s]));
+          }
+        }
+        stage = (stage + blocks) % kLinStages;
+      }
+    }
+  } else if (warp >= kLinEpiWarp0) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3, part = (warp - kLinEpiWarp0) / 4;
+    uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
+    int e = 0;
+    uint32_t used = 0;
+    for (int i = first; i < tiles; i += pairs) {
+      const LinTile t = tile_at(i, e);
+      e = t.e;
+      const int f0 = t.m0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's features on M
+      const bool none = depth_of(t) == 0;
+      if (none && p.accumulate) continue;
+      const uint32_t buf = used & 1;
+      if (!none) {
+        if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
+        tc_fence_after();
+      }
+      const uint32_t tq = tmem_base + buf * kLinTile + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+      for (int c0 = 32 * part; c0 < t.n && f0 < p.M; c0 += 64) {
+        float v[32];
+        if (none) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        } else {
+          tmem_ld16(tq + c0, v);
+          tmem_ld16(tq + c0 + 16, v + 16);
+          tmem_ld_wait();
+        }
+        if (DIR == kWgrad) {
+          // lane = row of D: its columns are adjacent in dW
+          const int left = p.C - (t.c0 + c0);  // columns from here on
+          auto row_at = [&](int r, int col, int size) -> uint8_t* {
+            if (f0 + r >= p.M) return nullptr;
+            return static_cast<uint8_t*>(p.out) +
+                   ((static_cast<long long>(t.e) * p.M + f0 + r) * p.ld + t.c0 + c0 + col) * size;
+          };
+          if (p.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<float4*>(tile + lane * 80 + j * 16) =
+                    make_float4(v[16 * h + 4 * j], v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2],
+                                v[16 * h + 4 * j + 3]);
+              __syncwarp();
+              auto at = [&](int r) { return row_at(r, 16 * h, 4); };
+              if (p.accumulate) store_rows64<true>(tile, lane, (left - 16 * h) * 4, at);
+              else store_rows64<false>(tile, lane, (left - 16 * h) * 4, at);
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = bf16_bits(v[8 * j + 2 * k]) | bf16_bits(v[8 * j + 2 * k + 1]) << 16;
+              *reinterpret_cast<uint4*>(tile + lane * 80 + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            store_rows64<false>(tile, lane, left * 2, [&](int r) { return row_at(r, 0, 2); });
+            __syncwarp();
+          }
+        } else {
+          // lane = feature, v = 32 token rows: the tile turns them into rows of 32 features
+          const int left = p.M - f0;
+          if (p.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 16 tokens at a time, rows of 128 bytes, 144 apart
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                *reinterpret_cast<float*>(tile + j * 144 + lane * 4) = v[16 * h + j];
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = lane / 8 + 4 * j, c = (lane & 7) * 4;
+                const int tok = c0 + 16 * h + r;
+                if (tok < t.cols && c < left) {
+                  float4 x = *reinterpret_cast<const float4*>(tile + r * 144 + c * 4);
+                  float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) +
+                                                        (t.c0 + tok) * p.ld + f0 + c);
+                  if (p.accumulate) {
+                    const float4 w = *o;
+                    x.x += w.x, x.y += w.y, x.z += w.z, x.w += w.w;
+                  }
+                  *o = x;
+                }
+              }
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint16_t*>(tile + j * 80 + lane * 2) =
+                  static_cast<uint16_t>(bf16_bits(v[j]));
+            __syncwarp();
+            store_rows64<false>(tile, lane, left * 2, [&](int r) -> uint8_t* {
+              if (c0 + r >= t.cols) return nullptr;
+              return static_cast<uint8_t*>(p.out) + ((t.c0 + c0 + r) * p.ld + f0) * 2;
+            });
+            __syncwarp();
+          }
+        }
+      }
+      if (!none) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&tempty[buf]);
+          else mbar_arrive_cluster(at_leader(&tempty[buf]));
+        }
+        ++used;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the other may still arrive on its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// CTA pairs that the device runs at once (a pair's two SMs lie in one cluster
+// of SMs, so this may be less than half the SMs); cached per device.
+template <int DIR>
+cudaError_t resident_pairs(int smem, int* pairs) {
+  static int cache[kMaxDevices] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (cache[dev] == 0) {
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof(lc));
+    lc.gridDim = dim3(num_sms() & ~1);
+    lc.blockDim = dim3(kLinThreads);
+    lc.dynamicSmemBytes = smem;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, grouped_linear<DIR>, &lc);
+    if (e != cudaSuccess) return e;
+    cache[dev] = n < 1 ? 1 : n;
+  }
+  *pairs = cache[dev];
+  return cudaSuccess;
+}
+
+template <int DIR>
+cudaError_t run(const moe_linear_desc& d, LinParams p, const LinMaps& m, cudaStream_t s) {
+  const int smem_max = kLinSmem + (2 * kMaxExpertsCfg + 2 + 33) * 4;
+  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(grouped_linear<DIR>), smem_max);
+  if (e != cudaSuccess) return e;
+  int pairs = 0;
+  if ((e = resident_pairs<DIR>(smem_max, &pairs)) != cudaSuccess) return e;
+  // no more pairs than tiles there can be
+  const long long most = DIR == kWgrad ? 1LL * d.E * p.mt * p.ct
+                                       : 1LL * p.mt * (cdiv(d.R, kLinTile) + (d.E < d.R ? d.E : d.R));
+  if (most < pairs) pairs = static_cast<int>(most);
+  return launch_pdl(grouped_linear<DIR>, dim3(2 * pairs), dim3(kLinThreads), smem_max, s, p, m);
 }
 
 }  // namespace
@@ -112,15 +518,39 @@ __global__ void __launch_bounds__(kThreads) linear_simple(const LinParams p) {
 cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const void* a,
                                   const void* b, const int32_t* offsets, void* out, int32_t* err,
                                   cudaStream_t s) {
-  LinParams p = {d.E, d.R, d.N, d.K, d.ld_x, d.ld_y, d.out_type == MOE_T_F32, d.accumulate != 0,
-                 static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), offsets, out, err};
-  const int cols = dir == kFwd ? d.N : d.K;
-  const int row_tiles = cdiv(d.R, kTile) + min(d.E, d.R);
-  const dim3 rows(row_tiles, cdiv(cols, kTile), 1), weights(cdiv(d.N, kTile), cdiv(cols, kTile), d.E);
-  if (dir == kFwd) linear_simple<kFwd><<<rows, kThreads, 0, s>>>(p);
-  else if (dir == kDgrad) linear_simple<kDgrad><<<rows, kThreads, 0, s>>>(p);
-  else linear_simple<kWgrad><<<weights, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  LinParams p;
+  memset(&p, 0, sizeof(p));
+  p.E = d.E;
+  p.R = d.R;
+  p.M = dir == kDgrad ? d.K : d.N;
+  p.C = dir == kWgrad ? d.K : 0;
+  p.depth = dir == kFwd ? d.K : d.N;
+  p.mt = cdiv(p.M, kLinTile);
+  p.ct = cdiv(p.C, kLinTile);
+  p.ld = dir == kFwd ? d.ld_y : dir == kDgrad ? d.ld_x : d.K;
+  p.out_f32 = d.out_type == MOE_T_F32;
+  p.accumulate = d.accumulate != 0;
+  p.offsets = offsets;
+  p.out = out;
+  p.err = err;
+  LinMaps m;
+  memset(&m, 0, sizeof(m));
+  bool ok = true;
+  if (dir == kWgrad) {
+    // no rows: every tile is empty and no map is read
+    if (d.R > 0)
+      ok = map_bf16_ld(&m.a, a, d.R, d.N, d.ld_y, 64) && map_bf16_ld(&m.b, b, d.R, d.K, d.ld_x, 64);
+  } else {
+    const int width = dir == kFwd ? d.K : d.N, ld = dir == kFwd ? d.ld_x : d.ld_y;
+    ok = map_bf16_blocks(&m.a, b, d.E, d.N, d.K, dir == kFwd ? 128 : 64) &&
+         map_bf16_ld(&m.b, a, d.R, width, ld, 128) && map_bf16_ld(&m.b32, a, d.R, width, ld, 32);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  switch (dir) {
+    case kFwd: return run<kFwd>(d, p, m, s);
+    case kDgrad: return run<kDgrad>(d, p, m, s);
+    default: return run<kWgrad>(d, p, m, s);
+  }
 }
 
 }  // namespace sgl

@@ -234,6 +234,16 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// The same for a 3D map.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m, uint32_t leader_bar,
+                                                 int c0, int c1, int c2, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(leader_bar), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -347,6 +357,20 @@ __device__ __forceinline__ uint64_t sdesc_k128(uint32_t saddr) {
   return d;
 }
 
+// The same for an MN-major tile: 64 consecutive M (or N) elements form a row
+// of 128 bytes, one row per contraction index, 128-byte swizzle. Eight rows
+// (contraction indices) are 1024 bytes (the stride byte offset), and the next
+// 64 M elements start `seg` bytes on (the leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t seg) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(seg >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
 // Block-scaled MMA, kind::mxf8f6f4: D (fp32, TMEM) (+)= (A * scaleA) x
 // (B * scaleB)^T over K = 32, A and B K-major 8-bit-per-element tiles in
 // shared memory (4-bit codes sit unpacked, 16 per 16 bytes), one e8m0 scale
@@ -388,6 +412,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+// Bits of an instruction descriptor that say A (B) is MN-major.
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 
 // Instruction descriptor, kind::mxf8f6f4 with e8m0 scales: A e2m1 (format 5)
 // and B e4m3 (format 0), both K-major; B's scale id at [4,6), formats at
