@@ -35,8 +35,8 @@
 // MMAs.
 //
 // Warp roles per CTA (384 threads):
-//   0      TMA producer (lane 0)
-//   1      TMEM allocation; MMA issuer (lane 0) in the leader
+//   0      TMA producer (one lane)
+//   1      TMEM allocation; MMA issuer (one lane) in the leader
 //   2      wgrad: zeroes the rows behind an expert's last
 //   3      idle
 //   4..11  epilogue, two warps per TMEM lane quarter, alternate column chunks
@@ -208,7 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pol = policy_evict_last(), pol_w = policy_evict_first();
       int stage = 0, e = 0;
       uint32_t phase = 0;
@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader && elect_one()) {
       constexpr uint32_t major = DIR == kFwd ? 0 : DIR == kDgrad ? kIdescMnA : kIdescMnA | kIdescMnB;
       int stage = 0, e = 0;
       uint32_t phase = 0, used = 0;  // used: accumulators taken so far

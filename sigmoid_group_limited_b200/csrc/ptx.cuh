@@ -13,6 +13,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a converged warp. The compiler knows that a block under
+// it runs in a single lane and feeds TMA and tcgen05 instructions their
+// (uniform) operands directly; under `lane == 0` it wraps each one in a loop
+// over the active lanes, which costs a tcgen05.mma 215 cycles whatever its
+// size, against 173 (M = 256, N = 256), 109 (N = 128) and 81 (N = 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------ programmatic dependent launch
 // Every kernel of the library is launched with programmatic stream
 // serialization (launch_pdl), so it may start while the kernel before it on
