@@ -56,14 +56,21 @@ namespace {
 
 constexpr int kLinThreads = 384;
 constexpr int kLinEpiWarp0 = 4, kLinEpiWarps = 8;
-constexpr int kLinStages = 6;
 constexpr int kLinHalf = 128 * 128;         // one operand's stage: 128 rows of 128 bytes
 constexpr int kLinStage = 2 * kLinHalf;     // A, B
 constexpr int kLinTile = 256;               // features on M, columns on N
-constexpr int kLinEpi = 32 * 80;            // a warp's transposition tile
 constexpr int kLinCtrl = 512;
-constexpr int kLinSmem = kLinStages * kLinStage + kLinEpiWarps * kLinEpi + kLinCtrl + 1024;
-static_assert(kLinSmem + (2 * kMaxExpertsCfg + 3 + 33) * 4 <= 227 * 1024, "shared memory");
+constexpr int kLinPitch = 80;               // a transposed row: 64 bytes, and 16 against conflicts
+constexpr int kLinBox = 32 * 128;           // a stored box of wgrad: 32 rows of 128 bytes
+
+// Per direction: pipeline stages, and a warp's share of the epilogue's shared memory.
+__host__ __device__ constexpr int lin_stages(int dir) { return dir == kWgrad ? 4 : 6; }
+__host__ __device__ constexpr int lin_epi(int dir) { return dir == kWgrad ? 2 * kLinBox : 32 * kLinPitch; }
+__host__ __device__ constexpr int lin_smem(int dir) {
+  return lin_stages(dir) * kLinStage + kLinEpiWarps * lin_epi(dir) + kLinCtrl + 1024 +
+         (2 * kMaxExpertsCfg + 2 + 33) * 4;
+}
+static_assert(lin_smem(kFwd) <= 227 * 1024 && lin_smem(kWgrad) <= 227 * 1024, "shared memory");
 
 struct LinParams {
   int E, R;
@@ -80,6 +87,7 @@ struct LinParams {
 struct LinMaps {
   CUtensorMap a;       // forward: W, 128-row boxes; dgrad: W, wgrad: dy, 64-row boxes
   CUtensorMap b, b32;  // forward, dgrad: rows, boxes of 128 and of 32; wgrad: x, 64-row boxes
+  CUtensorMap o;       // wgrad: dW, boxes of 32 rows of 128 bytes
 };
 
 struct LinTile {
@@ -88,31 +96,9 @@ struct LinTile {
   int n;           // MMA N: cols rounded up to 32
 };
 
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-  const __nv_bfloat16 b = __float2bfloat16(v);
-  return *reinterpret_cast<const uint16_t*>(&b);
-}
-
-// A warp's 32-row tile in shared memory (rows of 64 payload bytes, 80 apart)
-// to global memory: lane l moves 16 bytes of rows l / 4 + 8 i. `at(row)` is the
-// address of a row's first byte or null, `left` the payload bytes that exist.
-template <bool ADD, typename At>
-__device__ __forceinline__ void store_rows64(const uint8_t* tile, int lane, int left, At at) {
-  const int piece = (lane & 3) * 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = lane / 4 + 8 * i;
-    uint8_t* g = at(r);
-    if (g != nullptr && piece < left) {
-      float4 v = *reinterpret_cast<const float4*>(tile + r * 80 + piece);
-      float4* o = reinterpret_cast<float4*>(g + piece);
-      if (ADD) {
-        const float4 w = *o;
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-      }
-      *o = v;
-    }
-  }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
 
 template <int DIR>
@@ -121,8 +107,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
+  constexpr int kLinStages = lin_stages(DIR);
   uint8_t* epi = smem + kLinStages * kLinStage;
-  uint8_t* ctrl = epi + kLinEpiWarps * kLinEpi;
+  uint8_t* ctrl = epi + kLinEpiWarps * lin_epi(DIR);
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [stages] (the leader's count)
   uint64_t* empty = full + kLinStages;                 // [stages]
   uint64_t* tail = empty + kLinStages;                 // [stages] wgrad: a last block has landed
@@ -344,7 +331,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           __syncwarp();
           if (lane == 0) {
             if (leader) mbar_arrive(&full[s]);
-            else mbar_arrive_cluster(at_leader(&full[s]));
+            else {
+              fence_release_shared_cluster();
+              mbar_arrive_cluster_relaxed(at_leader(&full[s]));
+            }
           }
         }
         stage = (stage + blocks) % kLinStages;
@@ -353,9 +343,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   } else if (warp >= kLinEpiWarp0) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, part = (warp - kLinEpiWarp0) / 4;
-    uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
+    uint8_t* tile = epi + (warp - kLinEpiWarp0) * lin_epi(DIR);
     int e = 0;
-    uint32_t used = 0;
+    uint32_t used = 0, boxes = 0;
     for (int i = first; i < tiles; i += pairs) {
       const LinTile t = tile_at(i, e);
       e = t.e;
@@ -368,58 +358,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         tc_fence_after();
       }
       const uint32_t tq = tmem_base + buf * kLinTile + (static_cast<uint32_t>(q * 32) << 16);
+      if (DIR == kWgrad) {
+        // lane = row of D, whose columns are adjacent in dW: boxes of 32 rows
+        // x 128 bytes by TMA, two in turn. The box ends at dW's edges by itself.
+        const int wide = p.out_f32 ? 32 : 64;
 #pragma unroll 1
-      for (int c0 = 32 * part; c0 < t.n && f0 < p.M; c0 += 64) {
-        float v[32];
-        if (none) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        } else {
-          tmem_ld16(tq + c0, v);
-          tmem_ld16(tq + c0 + 16, v + 16);
-          tmem_ld_wait();
-        }
-        if (DIR == kWgrad) {
-          // lane = row of D: its columns are adjacent in dW
-          const int left = p.C - (t.c0 + c0);  // columns from here on
-          auto row_at = [&](int r, int col, int size) -> uint8_t* {
-            if (f0 + r >= p.M) return nullptr;
-            return static_cast<uint8_t*>(p.out) +
-                   ((static_cast<long long>(t.e) * p.M + f0 + r) * p.ld + t.c0 + c0 + col) * size;
+        for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
+          uint8_t* box = tile + (boxes++ & 1) * kLinBox;
+          if (elect_one()) bulk_wait_read<1>();
+          __syncwarp();
+          auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) =
+                make_uint4(x, y, z, w);
           };
-          if (p.out_f32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && p.out_f32) break;
+            float v[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            } else {
+              tmem_ld16(tq + c0 + 32 * h, v);
+              tmem_ld16(tq + c0 + 32 * h + 16, v + 16);
+              tmem_ld_wait();
+            }
+            if (p.out_f32) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+            } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<float4*>(tile + lane * 80 + j * 16) =
-                    make_float4(v[16 * h + 4 * j], v[16 * h + 4 * j + 1], v[16 * h + 4 * j + 2],
-                                v[16 * h + 4 * j + 3]);
-              __syncwarp();
-              auto at = [&](int r) { return row_at(r, 16 * h, 4); };
-              if (p.accumulate) store_rows64<true>(tile, lane, (left - 16 * h) * 4, at);
-              else store_rows64<false>(tile, lane, (left - 16 * h) * 4, at);
-              __syncwarp();
+                put(4 * h + j, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                    pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
             }
-          } else {
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+            if (p.accumulate) tma_add_3d(&m.o, box, t.c0 + c0, f0, t.e);
+            else tma_store_3d(&m.o, box, t.c0 + c0, f0, t.e);
+            bulk_commit();
+          }
+        }
+      } else {
+        const int left = p.M - f0;  // features that exist
+#pragma unroll 1
+        for (int c0 = 32 * part; c0 < t.cols && left > 0; c0 += 64) {
+          if (!p.out_f32) {
+            // 32 features x 32 token rows, read as 8 x 8 fragments and stored
+            // transposed: rows of 32 features
+            float v[2][16];
+            tmem_ld_16x32(tq + c0, v[0]);
+            tmem_ld_16x32(tq + (16u << 16) + c0, v[1]);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = bf16_bits(v[8 * j + 2 * k]) | bf16_bits(v[8 * j + 2 * k + 1]) << 16;
-              *reinterpret_cast<uint4*>(tile + lane * 80 + j * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              const uint32_t r[4] = {pack_bf16(v[0][4 * j], v[0][4 * j + 1]), pack_bf16(v[0][4 * j + 2], v[0][4 * j + 3]),
+                                     pack_bf16(v[1][4 * j], v[1][4 * j + 1]), pack_bf16(v[1][4 * j + 2], v[1][4 * j + 3])};
+              stmatrix4_trans(tile + (8 * j + (lane & 7)) * kLinPitch + (lane >> 3) * 16, r);
             }
             __syncwarp();
-            store_rows64<false>(tile, lane, left * 2, [&](int r) { return row_at(r, 0, 2); });
-            __syncwarp();
-          }
-        } else {
-          // lane = feature, v = 32 token rows: the tile turns them into rows of 32 features
-          const int left = p.M - f0;
-          if (p.out_f32) {
+            const int piece = lane & 3;
+            uint16_t* o = static_cast<uint16_t*>(p.out) + (t.c0 + c0 + lane / 4) * p.ld + f0 + piece * 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 16 tokens at a time, rows of 128 bytes, 144 apart
+            for (int j = 0; j < 4; ++j) {
+              const int r = lane / 4 + 8 * j;
+              if (c0 + r < t.cols && piece * 8 < left)
+                *reinterpret_cast<uint4*>(o + 8 * j * p.ld) =
+                    *reinterpret_cast<const uint4*>(tile + r * kLinPitch + piece * 16);
+            }
+            __syncwarp();
+          } else {
+            // lane = feature: 16 token rows at a time, rows of 128 bytes, 144 apart
+            float v[32];
+            tmem_ld16(tq + c0, v);
+            tmem_ld16(tq + c0 + 16, v + 16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 *reinterpret_cast<float*>(tile + j * 144 + lane * 4) = v[16 * h + j];
@@ -441,17 +460,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               }
               __syncwarp();
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              *reinterpret_cast<uint16_t*>(tile + j * 80 + lane * 2) =
-                  static_cast<uint16_t>(bf16_bits(v[j]));
-            __syncwarp();
-            store_rows64<false>(tile, lane, left * 2, [&](int r) -> uint8_t* {
-              if (c0 + r >= t.cols) return nullptr;
-              return static_cast<uint8_t*>(p.out) + ((t.c0 + c0 + r) * p.ld + f0) * 2;
-            });
-            __syncwarp();
           }
         }
       }
@@ -459,11 +467,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
+          // hands over tensor memory only, which the tcgen05 fence orders; a release
+          // at cluster scope would wait for this tile's global stores
           if (leader) mbar_arrive(&tempty[buf]);
-          else mbar_arrive_cluster(at_leader(&tempty[buf]));
+          else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
         }
         ++used;
       }
+    }
+    if (DIR == kWgrad) {
+      __syncwarp();
+      if (elect_one()) bulk_wait<0>();
     }
   }
   tc_fence_before();
@@ -501,7 +515,7 @@ cudaError_t resident_pairs(int smem, int* pairs) {
 
 template <int DIR>
 cudaError_t run(const moe_linear_desc& d, LinParams p, const LinMaps& m, cudaStream_t s) {
-  const int smem_max = kLinSmem + (2 * kMaxExpertsCfg + 2 + 33) * 4;
+  const int smem_max = lin_smem(DIR);
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(grouped_linear<DIR>), smem_max);
   if (e != cudaSuccess) return e;
   int pairs = 0;
@@ -538,8 +552,10 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
   bool ok = true;
   if (dir == kWgrad) {
     // no rows: every tile is empty and no map is read
+    ok = p.out_f32 ? map_f32_blocks(&m.o, out, d.E, d.N, d.K, 32)
+                   : map_bf16_blocks(&m.o, out, d.E, d.N, d.K, 32);
     if (d.R > 0)
-      ok = map_bf16_ld(&m.a, a, d.R, d.N, d.ld_y, 64) && map_bf16_ld(&m.b, b, d.R, d.K, d.ld_x, 64);
+      ok = ok && map_bf16_ld(&m.a, a, d.R, d.N, d.ld_y, 64) && map_bf16_ld(&m.b, b, d.R, d.K, d.ld_x, 64);
   } else {
     const int width = dir == kFwd ? d.K : d.N, ld = dir == kFwd ? d.ld_x : d.ld_y;
     ok = map_bf16_blocks(&m.a, b, d.E, d.N, d.K, dir == kFwd ? 128 : 64) &&
