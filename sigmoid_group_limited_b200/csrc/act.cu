@@ -81,8 +81,10 @@ __device__ __forceinline__ float row_weight(const ActParams& p, int r, long long
   return p.w[j];
 }
 
+// A group of G lanes owns a row, and each lane has U pieces of it under way.
 template <int G, bool BWD>
 __global__ void __launch_bounds__(kActThreads) act_kernel(const ActParams p) {
+  constexpr int U = 4;
   const int live = p.rows ? max(0, min(*p.rows, p.R)) : p.R;
   const int lane = threadIdx.x % G;
   const int per = kActThreads / G;
@@ -90,47 +92,78 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActParams p) {
     long long slot;
     const float w = row_weight(p, r, &slot);
     float sum = 0.f;
-#pragma unroll 4
-    for (int c = lane; c < p.chunks; c += G) {
-      float g[8], u[8], dh[8], o[8], o2[8];
-      unpack8(load8(p.g, r * p.ld_g + 8 * c), g);
-      unpack8(load8(p.u, r * p.ld_g + 8 * c), u);
-      if (BWD) unpack8(load8(p.dh, r * p.ld_h + 8 * c), dh);
+    for (int c0 = lane; c0 < p.chunks; c0 += G * U) {
+      uint4 qg[U], qu[U], qd[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = clamp_nan(g[i], p.limit), b = clamp_nan(u[i], p.limit);
-        const float s = sigmoid_fast(a);
-        const float silu = a * s;
-        if (!BWD) {
-          o[i] = w * silu * b;
-        } else {
-          sum += dh[i] * (silu * b);
-          const float wd = w * dh[i];
-          o[i] = fabsf(g[i]) > p.limit ? 0.f : wd * b * (s + silu * (1.f - s));
-          o2[i] = fabsf(u[i]) > p.limit ? 0.f : wd * silu;
+      for (int k = 0; k < U; ++k) {
+        const int c = c0 + k * G;
+        if (c < p.chunks) {
+          qg[k] = load8(p.g, r * p.ld_g + 8 * c);
+          qu[k] = load8(p.u, r * p.ld_g + 8 * c);
+          if (BWD) qd[k] = load8(p.dh, r * p.ld_h + 8 * c);
         }
       }
-      if (!BWD) {
-        store8(p.h, r * p.ld_h + 8 * c, pack8(o));
-      } else {
-        store8(p.dg, r * p.ld_dg + 8 * c, pack8(o));
-        store8(p.du, r * p.ld_dg + 8 * c, pack8(o2));
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int c = c0 + k * G;
+        if (c >= p.chunks) break;
+        float g[8], u[8], dh[8], o[8], o2[8];
+        unpack8(qg[k], g);
+        unpack8(qu[k], u);
+        if (BWD) unpack8(qd[k], dh);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = clamp_nan(g[i], p.limit), b = clamp_nan(u[i], p.limit);
+          const float s = sigmoid_fast(a);
+          const float silu = a * s;
+          if (!BWD) {
+            o[i] = w * silu * b;
+          } else {
+            sum += dh[i] * (silu * b);
+            const float wd = w * dh[i];
+            o[i] = fabsf(g[i]) > p.limit ? 0.f : wd * b * (s + silu * (1.f - s));
+            o2[i] = fabsf(u[i]) > p.limit ? 0.f : wd * silu;
+          }
+        }
+        if (!BWD) {
+          store8(p.h, r * p.ld_h + 8 * c, pack8(o));
+        } else {
+          store8(p.dg, r * p.ld_dg + 8 * c, pack8(o));
+          store8(p.du, r * p.ld_dg + 8 * c, pack8(o2));
+        }
       }
     }
     if (BWD && p.dw != nullptr) {
+      constexpr int W = G < 32 ? G : 32;
+      // the lanes of this row (other rows of the warp may have ended)
+      const uint32_t mask = W == 32 ? 0xffffffffu : ((1u << W) - 1u) << (threadIdx.x % 32 / W * W);
 #pragma unroll
-      for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(__activemask(), sum, o, G);
+      for (int o = W / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o, W);
+      if (G > 32) {  // the whole block is in this row
+        __shared__ float part[kActThreads / 32];
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int i = 0; i < kActThreads / 32; ++i) sum += part[i];
+      }
       if (lane == 0 && slot >= 0) p.dw[slot] = sum;
     }
   }
 }
 
+template <int G, bool BWD>
+cudaError_t launch_rows(const ActParams& p, cudaStream_t s) {
+  const int grid = min(cdiv(p.R, kActThreads / G), num_sms() * 8);
+  act_kernel<G, BWD><<<grid, kActThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <bool BWD>
 cudaError_t launch_act(const ActParams& p, cudaStream_t s) {
-  const int per = kActThreads / 32;
-  const int grid = min(cdiv(p.R, per), num_sms() * 8);
-  act_kernel<32, BWD><<<grid, kActThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (p.chunks <= 32) return launch_rows<8, BWD>(p, s);
+  if (p.chunks <= 256) return launch_rows<32, BWD>(p, s);
+  return launch_rows<kActThreads, BWD>(p, s);
 }
 
 ActParams common(const moe_swiglu_desc& d, const void* g, const void* u, const float* w,

@@ -311,9 +311,10 @@ bool map_bf16_ld(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, 
                  uint32_t box_rows);
 bool map_bf16_blocks(CUtensorMap* m, const void* ptr, uint64_t blocks, uint64_t rows,
                      uint64_t cols, uint32_t box_rows);
-// The blocks as fp32: boxes of 32 columns.
-bool map_f32_blocks(CUtensorMap* m, const void* ptr, uint64_t blocks, uint64_t rows, uint64_t cols,
-                    uint32_t box_rows);
+// The blocks as bf16 or fp32 to store to, in boxes of row_bytes (64 or 128) x
+// box_rows with the swizzle of that width.
+bool map_store_blocks(CUtensorMap* m, void* ptr, bool f32, uint64_t blocks, uint64_t rows,
+                      uint64_t cols, uint32_t box_rows, uint32_t row_bytes);
 // Row-major [rows, cols] bytes (e4m3 codes): box of box_rows x 128 bytes,
 // 128-byte swizzle.
 bool map_u8(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);

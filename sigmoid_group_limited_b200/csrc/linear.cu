@@ -34,6 +34,14 @@
 // Two 256-column accumulators: a tile's epilogue runs under the next tile's
 // MMAs.
 //
+// The tensor core's fp32 accumulation cuts low bits off at every step, always
+// towards zero: about 1.7e-8 of the sum per 16-deep step, 6e-6 at a depth of
+// 6000. A bf16 result does not see it. An fp32 result is made in passes of
+// 512: each pass starts a fresh accumulator and the epilogue adds it to the
+// output in fp32 (rounded to nearest), which holds the error at about 6e-7 at
+// any depth. The adds are reductions in L2 (one per element and pass, by the
+// same thread in order, so the result is the same every time).
+//
 // Warp roles per CTA (384 threads):
 //   0      TMA producer (one lane)
 //   1      TMEM allocation; MMA issuer (one lane) in the leader
@@ -59,18 +67,17 @@ constexpr int kLinEpiWarp0 = 4, kLinEpiWarps = 8;
 constexpr int kLinHalf = 128 * 128;         // one operand's stage: 128 rows of 128 bytes
 constexpr int kLinStage = 2 * kLinHalf;     // A, B
 constexpr int kLinTile = 256;               // features on M, columns on N
+constexpr int kLinChunk = 512;  // contraction per pass of an fp32 result, a multiple of 64
 constexpr int kLinCtrl = 512;
 constexpr int kLinPitch = 80;               // a transposed row: 64 bytes, and 16 against conflicts
-constexpr int kLinBox = 32 * 128;           // a stored box of wgrad: 32 rows of 128 bytes
+constexpr int kLinStages = 6;
+constexpr int kLinBoxRow = 64;              // a stored box of wgrad: 32 rows of 64 bytes
+constexpr int kLinBox = 32 * kLinBoxRow;
 
-// Per direction: pipeline stages, and a warp's share of the epilogue's shared memory.
-__host__ __device__ constexpr int lin_stages(int dir) { return dir == kWgrad ? 4 : 6; }
-__host__ __device__ constexpr int lin_epi(int dir) { return dir == kWgrad ? 2 * kLinBox : 32 * kLinPitch; }
-__host__ __device__ constexpr int lin_smem(int dir) {
-  return lin_stages(dir) * kLinStage + kLinEpiWarps * lin_epi(dir) + kLinCtrl + 1024 +
-         (2 * kMaxExpertsCfg + 2 + 33) * 4;
-}
-static_assert(lin_smem(kFwd) <= 227 * 1024 && lin_smem(kWgrad) <= 227 * 1024, "shared memory");
+constexpr int kLinEpi = 32 * kLinPitch > kLinBox ? 32 * kLinPitch : kLinBox;  // per epilogue warp
+constexpr int kLinSmem = kLinStages * kLinStage + kLinEpiWarps * kLinEpi + kLinCtrl + 1024 +
+                         (2 * kMaxExpertsCfg + 2 + 33) * 4;
+static_assert(kLinSmem <= 227 * 1024 && kLinEpi % 512 == 0, "shared memory");
 
 struct LinParams {
   int E, R;
@@ -87,7 +94,7 @@ struct LinParams {
 struct LinMaps {
   CUtensorMap a;       // forward: W, 128-row boxes; dgrad: W, wgrad: dy, 64-row boxes
   CUtensorMap b, b32;  // forward, dgrad: rows, boxes of 128 and of 32; wgrad: x, 64-row boxes
-  CUtensorMap o;       // wgrad: dW, boxes of 32 rows of 128 bytes
+  CUtensorMap o;       // wgrad: dW, boxes of 32 rows of kLinBoxRow bytes
 };
 
 struct LinTile {
@@ -101,15 +108,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// Adds 16 bytes of fp32 to global memory without reading them back.
+__device__ __forceinline__ void red_add_v4(float* p, const float4& v) {
+  asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
+               "f"(v.w)
+               : "memory");
+}
+
 template <int DIR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     grouped_linear(const __grid_constant__ LinParams p, const __grid_constant__ LinMaps m) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  constexpr int kLinStages = lin_stages(DIR);
   uint8_t* epi = smem + kLinStages * kLinStage;
-  uint8_t* ctrl = epi + kLinEpiWarps * lin_epi(DIR);
+  uint8_t* ctrl = epi + kLinEpiWarps * kLinEpi;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);  // [stages] (the leader's count)
   uint64_t* empty = full + kLinStages;                 // [stages]
   uint64_t* tail = empty + kLinStages;                 // [stages] wgrad: a last block has landed
@@ -191,6 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     t.n = (t.cols + 31) & ~31;
     return t;
   };
+  const int chunk = p.out_f32 ? kLinChunk : 1 << 30;  // contraction per accumulator
   auto depth_of = [&](const LinTile& t) { return DIR == kWgrad ? t.rows : p.depth; };
 
   if (warp == 0) {
@@ -277,13 +291,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         e = t.e;
         const int depth = depth_of(t);
         if (depth == 0) continue;
-        const uint32_t buf = used & 1, idesc = idesc_bf16(2 * 128, t.n) | major;
-        if (!mbar_wait_cluster(&tempty[buf], ((used >> 1) & 1) ^ 1, abort_flag, p.err,
-                               MOE_DEVERR_TIMEOUT))
-          break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + buf * kLinTile;
+        const uint32_t idesc = idesc_bf16(2 * 128, t.n) | major;
+        uint32_t d = 0;
         for (int k0 = 0; k0 < depth; k0 += 64) {
+          const bool fresh = k0 % chunk == 0;
+          if (fresh) {  // the next accumulator
+            if (k0 > 0) umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
+            const uint32_t buf = used & 1;
+            if (!mbar_wait_cluster(&tempty[buf], ((used >> 1) & 1) ^ 1, abort_flag, p.err,
+                                   MOE_DEVERR_TIMEOUT)) {
+              live = false;
+              break;
+            }
+            tc_fence_after();
+            d = tmem_base + buf * kLinTile;
+          }
           if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
             live = false;
             break;
@@ -294,14 +316,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           for (int k = 0; k < steps; ++k) {
             const uint64_t da = DIR == kFwd ? sdesc_k128(a0 + k * 32) : sdesc_mn128(a0 + k * 2048, 8192);
             const uint64_t db = DIR == kWgrad ? sdesc_mn128(b0 + k * 2048, 8192) : sdesc_k128(b0 + k * 32);
-            umma_bf16_pair(d, da, db, idesc, (k0 | k) != 0 ? 1u : 0u);
+            umma_bf16_pair(d, da, db, idesc, fresh && k == 0 ? 0u : 1u);
           }
           umma_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both CTAs
           if (++stage == kLinStages) stage = 0, phase ^= 1;
         }
         if (!live) break;
-        umma_commit_pair_mc(&tfull[buf], 0x3);
-        ++used;
+        umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
       }
     }
     __syncwarp();
@@ -343,137 +364,142 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   } else if (warp >= kLinEpiWarp0) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int q = warp & 3, part = (warp - kLinEpiWarp0) / 4;
-    uint8_t* tile = epi + (warp - kLinEpiWarp0) * lin_epi(DIR);
+    uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
     int e = 0;
-    uint32_t used = 0, boxes = 0;
+    uint32_t used = 0;
     for (int i = first; i < tiles; i += pairs) {
       const LinTile t = tile_at(i, e);
       e = t.e;
       const int f0 = t.m0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's features on M
-      const bool none = depth_of(t) == 0;
+      const int depth = depth_of(t);
+      const bool none = depth == 0;
       if (none && p.accumulate) continue;
-      const uint32_t buf = used & 1;
-      if (!none) {
-        if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
-        tc_fence_after();
-      }
-      const uint32_t tq = tmem_base + buf * kLinTile + (static_cast<uint32_t>(q * 32) << 16);
-      if (DIR == kWgrad) {
-        // lane = row of D, whose columns are adjacent in dW: boxes of 32 rows
-        // x 128 bytes by TMA, two in turn. The box ends at dW's edges by itself.
-        const int wide = p.out_f32 ? 32 : 64;
-#pragma unroll 1
-        for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
-          uint8_t* box = tile + (boxes++ & 1) * kLinBox;
-          if (elect_one()) bulk_wait_read<1>();
-          __syncwarp();
-          auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) =
-                make_uint4(x, y, z, w);
-          };
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1 && p.out_f32) break;
-            float v[32];
-            if (none) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            } else {
-              tmem_ld16(tq + c0 + 32 * h, v);
-              tmem_ld16(tq + c0 + 32 * h + 16, v + 16);
-              tmem_ld_wait();
-            }
-            if (p.out_f32) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                put(4 * h + j, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                    pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-            }
+      bool live = true;
+      for (int k0 = 0; k0 == 0 || k0 < depth; k0 += chunk) {
+        const bool add = p.accumulate || k0 > 0;
+        const uint32_t buf = used & 1;
+        if (!none) {
+          if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+            live = false;
+            break;
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (elect_one()) {
-            if (p.accumulate) tma_add_3d(&m.o, box, t.c0 + c0, f0, t.e);
-            else tma_store_3d(&m.o, box, t.c0 + c0, f0, t.e);
-            bulk_commit();
-          }
+          tc_fence_after();
         }
-      } else {
-        const int left = p.M - f0;  // features that exist
+        // the pass before has reached the output (bulk stores keep no order)
+        if (DIR == kWgrad && k0 > 0 && elect_one()) bulk_wait<0>();
+        const uint32_t tq = tmem_base + buf * kLinTile + (static_cast<uint32_t>(q * 32) << 16);
+        if (DIR == kWgrad) {
+          // lane = row of D, whose columns are adjacent in dW: boxes of 32 rows
+          // by TMA. The box ends at dW's edges by itself.
+          const int wide = kLinBoxRow / (p.out_f32 ? 4 : 2);
 #pragma unroll 1
-        for (int c0 = 32 * part; c0 < t.cols && left > 0; c0 += 64) {
-          if (!p.out_f32) {
-            // 32 features x 32 token rows, read as 8 x 8 fragments and stored
-            // transposed: rows of 32 features
-            float v[2][16];
-            tmem_ld_16x32(tq + c0, v[0]);
-            tmem_ld_16x32(tq + (16u << 16) + c0, v[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t r[4] = {pack_bf16(v[0][4 * j], v[0][4 * j + 1]), pack_bf16(v[0][4 * j + 2], v[0][4 * j + 3]),
-                                     pack_bf16(v[1][4 * j], v[1][4 * j + 1]), pack_bf16(v[1][4 * j + 2], v[1][4 * j + 3])};
-              stmatrix4_trans(tile + (8 * j + (lane & 7)) * kLinPitch + (lane >> 3) * 16, r);
-            }
+          for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
+            if (elect_one()) bulk_wait_read<0>();  // the warp's box is free again
             __syncwarp();
-            const int piece = lane & 3;
-            uint16_t* o = static_cast<uint16_t*>(p.out) + (t.c0 + c0 + lane / 4) * p.ld + f0 + piece * 8;
+            auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+              const int at = piece ^ ((lane >> 1) & 3);  // the 64-byte swizzle
+              *reinterpret_cast<uint4*>(tile + lane * kLinBoxRow + (at << 4)) = make_uint4(x, y, z, w);
+            };
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int r = lane / 4 + 8 * j;
-              if (c0 + r < t.cols && piece * 8 < left)
-                *reinterpret_cast<uint4*>(o + 8 * j * p.ld) =
-                    *reinterpret_cast<const uint4*>(tile + r * kLinPitch + piece * 16);
+            for (int h = 0; h < 2; ++h) {  // 16 columns at a time
+              if (p.out_f32 && h == 1) break;
+              float v[16];
+              if (none) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0.f;
+              } else {
+                tmem_ld16(tq + c0 + 16 * h, v);
+                tmem_ld_wait();
+              }
+              if (p.out_f32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  put(4 * h + j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                      __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  put(2 * h + j, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+              }
             }
+            fence_proxy_async_smem();
             __syncwarp();
-          } else {
-            // lane = feature: 16 token rows at a time, rows of 128 bytes, 144 apart
-            float v[32];
-            tmem_ld16(tq + c0, v);
-            tmem_ld16(tq + c0 + 16, v + 16);
-            tmem_ld_wait();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<float*>(tile + j * 144 + lane * 4) = v[16 * h + j];
-              __syncwarp();
+            if (elect_one()) {
+              if (add) tma_add_3d(&m.o, tile, t.c0 + c0, f0, t.e);
+              else tma_store_3d(&m.o, tile, t.c0 + c0, f0, t.e);
+              bulk_commit();
+            }
+          }
+        } else {
+          const int left = p.M - f0;  // features that exist
+#pragma unroll 1
+          for (int c0 = 32 * part; c0 < t.cols && left > 0; c0 += 64) {
+            if (!p.out_f32) {
+              // 32 features x 32 token rows, read as 8 x 8 fragments and stored
+              // transposed: rows of 32 features
+              float v[2][16];
+              tmem_ld_16x32(tq + c0, v[0]);
+              tmem_ld_16x32(tq + (16u << 16) + c0, v[1]);
+              tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int r = lane / 8 + 4 * j, c = (lane & 7) * 4;
-                const int tok = c0 + 16 * h + r;
-                if (tok < t.cols && c < left) {
-                  float4 x = *reinterpret_cast<const float4*>(tile + r * 144 + c * 4);
-                  float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) +
-                                                        (t.c0 + tok) * p.ld + f0 + c);
-                  if (p.accumulate) {
-                    const float4 w = *o;
-                    x.x += w.x, x.y += w.y, x.z += w.z, x.w += w.w;
-                  }
-                  *o = x;
-                }
+                const uint32_t r[4] = {pack_bf16(v[0][4 * j], v[0][4 * j + 1]), pack_bf16(v[0][4 * j + 2], v[0][4 * j + 3]),
+                                       pack_bf16(v[1][4 * j], v[1][4 * j + 1]), pack_bf16(v[1][4 * j + 2], v[1][4 * j + 3])};
+                stmatrix4_trans(tile + (8 * j + (lane & 7)) * kLinPitch + (lane >> 3) * 16, r);
               }
               __syncwarp();
+              const int piece = lane & 3;
+              uint16_t* o = static_cast<uint16_t*>(p.out) + (t.c0 + c0 + lane / 4) * p.ld + f0 + piece * 8;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int r = lane / 4 + 8 * j;
+                if (c0 + r < t.cols && piece * 8 < left)
+                  *reinterpret_cast<uint4*>(o + 8 * j * p.ld) =
+                      *reinterpret_cast<const uint4*>(tile + r * kLinPitch + piece * 16);
+              }
+              __syncwarp();
+            } else {
+              // lane = feature: 16 token rows at a time, rows of 128 bytes, 144 apart
+              float v[32];
+              tmem_ld16(tq + c0, v);
+              tmem_ld16(tq + c0 + 16, v + 16);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  *reinterpret_cast<float*>(tile + j * 144 + lane * 4) = v[16 * h + j];
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int r = lane / 8 + 4 * j, c = (lane & 7) * 4;
+                  const int tok = c0 + 16 * h + r;
+                  if (tok < t.cols && c < left) {
+                    const float4 x = *reinterpret_cast<const float4*>(tile + r * 144 + c * 4);
+                    float* o = static_cast<float*>(p.out) + (t.c0 + tok) * p.ld + f0 + c;
+                    if (add) red_add_v4(o, x);
+                    else *reinterpret_cast<float4*>(o) = x;
+                  }
+                }
+                __syncwarp();
+              }
             }
           }
         }
-      }
-      if (!none) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          // hands over tensor memory only, which the tcgen05 fence orders; a release
-          // at cluster scope would wait for this tile's global stores
-          if (leader) mbar_arrive(&tempty[buf]);
-          else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
+        if (!none) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            // hands over tensor memory only, which the tcgen05 fence orders; a release
+            // at cluster scope would wait for this tile's global stores
+            if (leader) mbar_arrive(&tempty[buf]);
+            else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
+          }
+          ++used;
         }
-        ++used;
       }
+      if (!live) break;
     }
     if (DIR == kWgrad) {
       __syncwarp();
@@ -515,16 +541,15 @@ cudaError_t resident_pairs(int smem, int* pairs) {
 
 template <int DIR>
 cudaError_t run(const moe_linear_desc& d, LinParams p, const LinMaps& m, cudaStream_t s) {
-  const int smem_max = lin_smem(DIR);
-  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(grouped_linear<DIR>), smem_max);
+  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(grouped_linear<DIR>), kLinSmem);
   if (e != cudaSuccess) return e;
   int pairs = 0;
-  if ((e = resident_pairs<DIR>(smem_max, &pairs)) != cudaSuccess) return e;
+  if ((e = resident_pairs<DIR>(kLinSmem, &pairs)) != cudaSuccess) return e;
   // no more pairs than tiles there can be
   const long long most = DIR == kWgrad ? 1LL * d.E * p.mt * p.ct
                                        : 1LL * p.mt * (cdiv(d.R, kLinTile) + (d.E < d.R ? d.E : d.R));
   if (most < pairs) pairs = static_cast<int>(most);
-  return launch_pdl(grouped_linear<DIR>, dim3(2 * pairs), dim3(kLinThreads), smem_max, s, p, m);
+  return launch_pdl(grouped_linear<DIR>, dim3(2 * pairs), dim3(kLinThreads), kLinSmem, s, p, m);
 }
 
 }  // namespace
@@ -552,8 +577,7 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
   bool ok = true;
   if (dir == kWgrad) {
     // no rows: every tile is empty and no map is read
-    ok = p.out_f32 ? map_f32_blocks(&m.o, out, d.E, d.N, d.K, 32)
-                   : map_bf16_blocks(&m.o, out, d.E, d.N, d.K, 32);
+    ok = map_store_blocks(&m.o, out, p.out_f32 != 0, d.E, d.N, d.K, 32, kLinBoxRow);
     if (d.R > 0)
       ok = ok && map_bf16_ld(&m.a, a, d.R, d.N, d.ld_y, 64) && map_bf16_ld(&m.b, b, d.R, d.K, d.ld_x, 64);
   } else {

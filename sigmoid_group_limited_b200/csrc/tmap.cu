@@ -59,16 +59,18 @@ bool map_bf16_blocks(CUtensorMap* m, const void* ptr, uint64_t blocks, uint64_t 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool map_f32_blocks(CUtensorMap* m, const void* ptr, uint64_t blocks, uint64_t rows, uint64_t cols,
-                    uint32_t box_rows) {
+bool map_store_blocks(CUtensorMap* m, void* ptr, bool f32, uint64_t blocks, uint64_t rows,
+                      uint64_t cols, uint32_t box_rows, uint32_t row_bytes) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || ptr == nullptr || rows == 0 || blocks == 0) return false;
+  const uint32_t size = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {cols, rows, blocks};
-  const cuuint64_t strides[2] = {cols * 4, rows * cols * 4};
-  const cuuint32_t box[3] = {32, box_rows, 1};
+  const cuuint64_t strides[2] = {cols * size, rows * cols * size};
+  const cuuint32_t box[3] = {row_bytes / size, box_rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(ptr), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr,
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
