@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace sgl {
 namespace {
@@ -60,12 +61,17 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, long long at) {
 __device__ __forceinline__ void store8(uint16_t* p, long long at, const uint4& v) {
   *reinterpret_cast<uint4*>(p + at) = v;
 }
-// The limit as comparisons, which keep a NaN (fminf / fmaxf would drop it).
+// The limit, keeping a NaN (fminf / fmaxf would drop it).
 __device__ __forceinline__ float clamp_nan(float v, float L) {
-  return v > L ? L : (v < -L ? -L : v);
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(L));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-L));
+  return r;
 }
 __device__ __forceinline__ float sigmoid_fast(float a) {
-  return __fdividef(1.f, 1.f + __expf(-a));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-a)));
+  return r;
 }
 
 // Routing weight of row r and where its gradient goes (-1: nowhere).
@@ -81,10 +87,12 @@ __device__ __forceinline__ float row_weight(const ActParams& p, int r, long long
   return p.w[j];
 }
 
-// A group of G lanes owns a row, and each lane has U pieces of it under way.
+// A group of G lanes owns a row, and each lane has U pieces of it under way:
+// with four blocks to an SM about 100 KB of loads.
 template <int G, bool BWD>
-__global__ void __launch_bounds__(kActThreads) act_kernel(const ActParams p) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(kActThreads, 4) act_kernel(const ActParams p) {
+  constexpr int U = BWD ? 2 : 4;
+  pdl_wait();
   const int live = p.rows ? max(0, min(*p.rows, p.R)) : p.R;
   const int lane = threadIdx.x % G;
   const int per = kActThreads / G;
@@ -155,8 +163,7 @@ __global__ void __launch_bounds__(kActThreads) act_kernel(const ActParams p) {
 template <int G, bool BWD>
 cudaError_t launch_rows(const ActParams& p, cudaStream_t s) {
   const int grid = min(cdiv(p.R, kActThreads / G), num_sms() * 8);
-  act_kernel<G, BWD><<<grid, kActThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(act_kernel<G, BWD>, dim3(grid), dim3(kActThreads), 0, s, p);
 }
 
 template <bool BWD>

@@ -10,6 +10,9 @@ using namespace sgl;
 
 namespace {
 
+// The calls launch with programmatic stream serialization: their kernels wait
+// for the kernel before them at once and never release the next one early, so
+// only the launch latency overlaps (2 us of a 30 us SwiGLU).
 constexpr int kMaxRows = 1 << 25;
 constexpr int kMaxFeatures = 16384;
 
@@ -38,7 +41,7 @@ bool swiglu_ok(const moe_swiglu_desc* d, bool backward) {
 
 moe_status grouped(const moe_linear_desc* d, LinearDir dir, const void* a, const void* b,
                    const int32_t* offsets, void* out, void* ws, size_t ws_bytes, void* stream) {
-  PdlScope pdl_scope(kPdlMaxTokens + 1);  // plain launches
+  PdlScope pdl_scope(0);  // programmatic dependent launch
   if (!linear_ok(d)) return MOE_ERR_CFG;
   // row-wise tensors without rows may have no address: a, and out or (wgrad) b
   const bool rows = d->R > 0, wg = dir == kWgrad;
@@ -94,6 +97,7 @@ moe_status moe_linear_read_error(void* ws, size_t ws_bytes, void* stream, int32_
 moe_status moe_swiglu(const moe_swiglu_desc* desc, const void* g, const void* u, const float* w,
                       const int32_t* perm, int32_t n_w, const int32_t* rows, void* h,
                       void* stream) {
+  PdlScope pdl_scope(0);
   if (!swiglu_ok(desc, false)) return MOE_ERR_CFG;
   if (w != nullptr && perm != nullptr && n_w < 0) return MOE_ERR_CFG;
   if (desc->R > 0 && (!g || !u || !h)) return MOE_ERR_NULL;
@@ -108,6 +112,7 @@ moe_status moe_swiglu(const moe_swiglu_desc* desc, const void* g, const void* u,
 moe_status moe_swiglu_backward(const moe_swiglu_desc* desc, const void* dh, const void* g,
                                const void* u, const float* w, const int32_t* perm, int32_t n_w,
                                const int32_t* rows, void* dg, void* du, float* dw, void* stream) {
+  PdlScope pdl_scope(0);
   if (!swiglu_ok(desc, true)) return MOE_ERR_CFG;
   if (w != nullptr && perm != nullptr && n_w < 0) return MOE_ERR_CFG;
   if (dw && !w) return MOE_ERR_NULL;
@@ -124,6 +129,7 @@ moe_status moe_swiglu_backward(const moe_swiglu_desc* desc, const void* dh, cons
 
 moe_status moe_adamw_step(const moe_adamw_cfg* cfg, const moe_adamw_tensor* tensors,
                           int32_t n_tensors, void* stream) {
+  PdlScope pdl_scope(0);
   if (cfg == nullptr || n_tensors < 0) return MOE_ERR_CFG;
   if (n_tensors > 0 && tensors == nullptr) return MOE_ERR_NULL;
   // written so that a NaN fails its test

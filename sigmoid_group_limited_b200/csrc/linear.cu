@@ -36,9 +36,9 @@
 //
 // The tensor core's fp32 accumulation cuts low bits off at every step, always
 // towards zero: about 1.7e-8 of the sum per 16-deep step, 6e-6 at a depth of
-// 6000. A bf16 result does not see it. An fp32 result is made in passes of
-// 512: each pass starts a fresh accumulator and the epilogue adds it to the
-// output in fp32 (rounded to nearest), which holds the error at about 6e-7 at
+// 6000. A bf16 result does not see it. An fp32 result is made in passes of at
+// most 768: each pass starts a fresh accumulator and the epilogue adds it to the
+// output in fp32 (rounded to nearest), which holds the error at about 8e-7 at
 // any depth. The adds are reductions in L2 (one per element and pass, by the
 // same thread in order, so the result is the same every time).
 //
@@ -67,7 +67,7 @@ constexpr int kLinEpiWarp0 = 4, kLinEpiWarps = 8;
 constexpr int kLinHalf = 128 * 128;         // one operand's stage: 128 rows of 128 bytes
 constexpr int kLinStage = 2 * kLinHalf;     // A, B
 constexpr int kLinTile = 256;               // features on M, columns on N
-constexpr int kLinChunk = 512;  // contraction per pass of an fp32 result, a multiple of 64
+constexpr int kLinChunk = 768;  // most contraction per pass of an fp32 result
 constexpr int kLinCtrl = 512;
 constexpr int kLinPitch = 80;               // a transposed row: 64 bytes, and 16 against conflicts
 constexpr int kLinStages = 6;
@@ -163,6 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
+  pdl_wait();  // what follows reads and writes what earlier kernels wrote
   for (int i = tid; i <= p.E; i += kLinThreads) s_off[i] = p.offsets[i];
   tc_fence_before();
   __syncthreads();
@@ -204,7 +205,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     t.n = (t.cols + 31) & ~31;
     return t;
   };
-  const int chunk = p.out_f32 ? kLinChunk : 1 << 30;  // contraction per accumulator
+  // contraction per accumulator: equal shares, in whole 64-deep blocks
+  auto chunk_of = [&](int depth) {
+    if (!p.out_f32 || depth <= kLinChunk) return 1 << 30;
+    const int blocks = (depth + 63) / 64, passes = (depth + kLinChunk - 1) / kLinChunk;
+    return (blocks + passes - 1) / passes * 64;
+  };
   auto depth_of = [&](const LinTile& t) { return DIR == kWgrad ? t.rows : p.depth; };
 
   if (warp == 0) {
@@ -292,6 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const int depth = depth_of(t);
         if (depth == 0) continue;
         const uint32_t idesc = idesc_bf16(2 * 128, t.n) | major;
+        const int chunk = chunk_of(depth);
         uint32_t d = 0;
         for (int k0 = 0; k0 < depth; k0 += 64) {
           const bool fresh = k0 % chunk == 0;
@@ -373,6 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const int f0 = t.m0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's features on M
       const int depth = depth_of(t);
       const bool none = depth == 0;
+      const int chunk = chunk_of(depth);
       if (none && p.accumulate) continue;
       bool live = true;
       for (int k0 = 0; k0 == 0 || k0 < depth; k0 += chunk) {
