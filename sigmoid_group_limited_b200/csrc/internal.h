@@ -292,6 +292,10 @@ enum LinearDir { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const void* a,
                                   const void* b, const int32_t* offsets, void* out, int32_t* err,
                                   cudaStream_t s);
+// The forward product of at most kFewMaxRows rows (linear_few.cu).
+constexpr int kFewMaxRows = 128;
+cudaError_t launch_linear_few(const moe_linear_desc& d, const void* x, const void* W,
+                              const int32_t* offsets, void* y, int32_t* err, cudaStream_t s);
 cudaError_t launch_swiglu(const moe_swiglu_desc& d, const void* g, const void* u, const float* w,
                           const int32_t* perm, int n_w, const int32_t* rows, void* h,
                           cudaStream_t s);

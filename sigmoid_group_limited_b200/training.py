@@ -65,7 +65,7 @@ def declare(L) -> None:
 
 def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16):
     """(rows, width, row stride) of a row-wise tensor."""
-    if t.dim() != 2 or t.dtype != dtype:
+    if t.dtype is not dtype or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-d {dtype} tensor")
     n, w = t.shape
     ld, one = t.stride()
@@ -79,26 +79,31 @@ def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16):
 def _flat(t: Optional[torch.Tensor], name: str, dtype, n: Optional[int] = None, at_least: bool = False):
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor")
     if n is not None and (t.numel() < n if at_least else t.numel() != n):
         raise ValueError(f"{name}: has {t.numel()} elements, {n} are wanted")
     return t.data_ptr()
 
 
+def _current_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same handle without building a Stream object at every call, where torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _call(fn, where: str, tensors, stream, *args) -> None:
     """fn(*args, stream) on the tensors' device; None among them is skipped."""
-    dev = None
+    dev = tensors[0].get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
     for t in tensors:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError("expected a CUDA tensor")
-            if dev is None:
-                dev = t.device.index
-            elif t.device.index != dev:
-                raise ValueError("the tensors lie on different devices")
+        if t is not None and t.get_device() != dev:
+            raise ValueError("expected CUDA tensors of one device")
     if stream is None:
-        s = torch.cuda.current_stream(dev).cuda_stream
+        s = _current_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if dev != torch.cuda.current_device():
