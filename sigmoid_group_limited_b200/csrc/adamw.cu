@@ -7,9 +7,9 @@
 // list of all tensors' 256-element blocks, a warp per block (8 elements, 16
 // bytes of bf16, per lane), so a block's maximum for the 8-bit scales is one
 // warp reduction and nothing is read twice. No atomics: an element is owned
-// by one lane. The arithmetic of 8-bit states fills most of the issue slots
-// (44 instructions an element), so it is kept short: the scales go into the
-// moments' coefficients, and roots and reciprocals are the hardware's.
+// by one lane. The arithmetic of 8-bit states fills most of the issue slots, so
+// it is kept short: roots and reciprocals are the hardware's wherever they do
+// not decide a code.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -60,16 +60,16 @@ struct AdamParams {
 static_assert(sizeof(AdamParams<kManyTensors>) <= 32764, "kernel parameters");
 
 // A lane's piece of 8 elements of B bytes as 2 B words. Of a tensor's last
-// block only n of the 8 exist; the others read as zero and are not written.
+// block (not FULL) only n of the 8 exist; the others read as zero and are not
+// written.
 template <int B>
 struct Piece {
   uint32_t w[2 * B];
 };
-template <int B>
-__device__ __forceinline__ Piece<B> load_piece(const void* base, long long at, int n) {
+template <int B, bool FULL>
+__device__ __forceinline__ Piece<B> load_piece(const uint8_t* p, int n) {
   Piece<B> r;
-  const uint8_t* p = static_cast<const uint8_t*>(base) + at * B;
-  if (n == 8) {
+  if (FULL) {
     if (B == 1) {
       const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
       r.w[0] = v.x, r.w[1] = v.y;
@@ -93,10 +93,9 @@ __device__ __forceinline__ Piece<B> load_piece(const void* base, long long at, i
   }
   return r;
 }
-template <int B>
-__device__ __forceinline__ void store_piece(void* base, long long at, int n, const Piece<B>& r) {
-  uint8_t* p = static_cast<uint8_t*>(base) + at * B;
-  if (n == 8) {
+template <int B, bool FULL>
+__device__ __forceinline__ void store_piece(uint8_t* p, int n, const Piece<B>& r) {
+  if (FULL) {
     if (B == 1) {
       __stcs(reinterpret_cast<uint2*>(p), make_uint2(r.w[0], r.w[1]));
     } else {
@@ -165,38 +164,62 @@ __device__ __forceinline__ float rcp_fast(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// The codes of 8 values of a block whose scale this also writes. ROOT: the
-// values are square roots, none negative, and what is not zero gets at least
-// the smallest code.
-template <bool ROOT>
-__device__ __forceinline__ void store_codes(void* base, float* scale, long long at, int n,
-                                            const float* f) {
+// The largest of 8 magnitudes of every lane (they compare as integers, and a
+// NaN is larger than everything).
+__device__ __forceinline__ float warp_max(const float* f) {
   float top = fabsf(f[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(f[i]));
-  // magnitudes compare as integers, and a NaN is larger than everything
-  const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu));
-  const bool tiny = big < 7.888609052210118e-31f;  // 2^-100: 448 / big stays finite
-  const float inv = tiny ? 0.f : __fdividef(448.f, big);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu));
+}
+// The scales of a block's moments for their largest magnitudes, and the
+// factors of their codes: lane 0 works on m, lane 1 on v.
+__device__ __forceinline__ float2 write_scales(float* m_scale, float* v_scale, float top_m, float top_v) {
+  const int lane = threadIdx.x & 31;
+  const float top = lane == 0 ? top_m : top_v;
+  const bool tiny = top < 7.888609052210118e-31f;  // 2^-100: the factor stays finite
+  // an infinite or NaN maximum makes the scale, and with it the block, NaN
+  if (lane < 2)
+    *(lane == 0 ? m_scale : v_scale) =
+        tiny ? 0.f : (top <= 3.402823466e+38f ? top * (1.f / 448.f) : __int_as_float(0x7fc00000));
+  const float inv = tiny ? 0.f : __frcp_rn(top) * 448.f;
+  return make_float2(__shfl_sync(0xffffffffu, inv, 0), __shfl_sync(0xffffffffu, inv, 1));
+}
+__device__ __forceinline__ Piece<1> to_codes(const float* y) {
   Piece<1> r = {{0, 0}};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    r.w[i / 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv),
+    r.w[i / 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y[2 * i], y[2 * i + 1]),
                                                                  __NV_SATFINITE, __NV_E4M3))
                   << (16 * (i & 1));
-  if (ROOT) {
-    // a zero byte in one of the words (rare): is its value zero, too?
-    const uint32_t z = ((r.w[0] - 0x01010101u) & ~r.w[0]) | ((r.w[1] - 0x01010101u) & ~r.w[1]);
-    if ((z & 0x80808080u) != 0 && !tiny) {
+  return r;
+}
+// Codes of the square roots of 8 second moments. root: within an ulp or two,
+// enough for a code unless the value lies at a border between two codes;
+// there (low 19 mantissa bits near zero, 1 of 30000 values) the exact root
+// decides, so that the codes are those of the definition. What is not zero
+// gets at least the smallest code.
+__device__ __forceinline__ Piece<1> root_codes(const float* v, const float* root, float inv) {
+  float y[8];
+  uint32_t near = 0x7ffffu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (f[i] > 0.f && (r.w[i / 4] >> (8 * (i & 3)) & 0xffu) == 0) r.w[i / 4] |= 1u << (8 * (i & 3));
-    }
+  for (int i = 0; i < 8; ++i) {
+    y[i] = root[i] * inv;
+    near = min(near, (__float_as_uint(y[i]) + 8u) & 0x7ffffu);
   }
-  store_piece<1>(base, at, n, r);
-  // an infinite or NaN maximum makes the scale, and with it the block, NaN
-  if ((threadIdx.x & 31) == 0)
-    *scale = tiny ? 0.f : (big <= 3.402823466e+38f ? big / 448.f : __int_as_float(0x7fc00000));
+  if (near < 16u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fsqrt_rn(v[i]) * inv;
+  }
+  Piece<1> r = to_codes(y);
+  // a zero byte in one of the words (rare): is its value zero, too?
+  const uint32_t z = ((r.w[0] - 0x01010101u) & ~r.w[0]) | ((r.w[1] - 0x01010101u) & ~r.w[1]);
+  if ((z & 0x80808080u) != 0 && inv != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (y[i] > 0.f && (r.w[i / 4] >> (8 * (i & 3)) & 0xffu) == 0) r.w[i / 4] |= 1u << (8 * (i & 3));
+  }
+  return r;
 }
 
 struct AdamStep {
@@ -205,75 +228,101 @@ struct AdamStep {
   float cg, cgg;         // (1 - beta1) and (1 - beta2) with the gradient scale and its square
 };
 
-// Blocks [blk, end) of one tensor; PF32, MASTER, GF32, Q8: its types. The next
-// block's loads are under way while a block is computed.
-template <bool PF32, bool MASTER, bool GF32, bool Q8>
-__device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamStep& h,
-                                            long long blk, long long end, int lane) {
+// `count` blocks of one tensor from blk on, all of them whole (FULL) or the one
+// short block at its end; PF32, MASTER, GF32, Q8: its types. With 8-bit states
+// the next block's loads are under way while a block is computed.
+template <bool PF32, bool MASTER, bool GF32, bool Q8, bool FULL>
+__device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamStep& h, long long blk, int count,
+                                         int lane) {
+  constexpr int BP = PF32 ? 4 : 2, BG = GF32 ? 4 : 2, BS = Q8 ? 1 : 4;
   struct Block {
-    Piece<PF32 || MASTER ? 4 : 2> p;
-    Piece<GF32 ? 4 : 2> g;
-    Piece<Q8 ? 1 : 4> m, v;
-    float sm, sv;
-    int n;
+    Piece<MASTER ? 4 : BP> p;
+    Piece<BG> g;
+    Piece<BS> m, v;
+    float sm = 0.f, sv = 0.f;
   };
+  const long long at = blk * kBlock + lane * 8;
+  const int n = FULL ? 8 : static_cast<int>(max(0LL, min(8LL, t.n - at)));
+  uint8_t* pp = static_cast<uint8_t*>(t.p) + at * BP;
+  uint8_t* pw = MASTER ? reinterpret_cast<uint8_t*>(t.master + at) : pp;
+  const uint8_t* pg = static_cast<const uint8_t*>(t.g) + at * BG;
+  uint8_t *pm = static_cast<uint8_t*>(t.m) + at * BS, *pv = static_cast<uint8_t*>(t.v) + at * BS;
+  float *ps = t.m_scale + blk, *pr = t.v_scale + blk;
   const float keep = 1.f - h.lr * t.wd;
-  auto load = [&](long long b) {
+  auto load = [&](int j) {  // block j from here on
     Block k;
-    const long long at = b * kBlock + lane * 8;
-    k.n = static_cast<int>(max(0LL, min(8LL, t.n - at)));
-    k.m = load_piece<Q8 ? 1 : 4>(t.m, at, k.n);
-    k.v = load_piece<Q8 ? 1 : 4>(t.v, at, k.n);
-    k.g = load_piece<GF32 ? 4 : 2>(t.g, at, k.n);
-    k.p = load_piece<PF32 || MASTER ? 4 : 2>(MASTER ? t.master : t.p, at, k.n);
-    if (Q8) k.sm = t.m_scale[b], k.sv = t.v_scale[b];
+    k.m = load_piece<BS, FULL>(pm + j * (kBlock * BS), n);
+    k.v = load_piece<BS, FULL>(pv + j * (kBlock * BS), n);
+    k.g = load_piece<BG, FULL>(pg + j * (kBlock * BG), n);
+    k.p = load_piece<MASTER ? 4 : BP, FULL>(pw + j * (kBlock * (MASTER ? 4 : BP)), n);
+    if (Q8) k.sm = ps[j], k.sv = pr[j];
     return k;
   };
-  Block next = load(blk);
+  Block next;
+  if (Q8) next = load(0);
 #pragma unroll 1
-  for (; blk < end; ++blk) {
-    const Block k = next;
-    if (Q8 && blk + 1 < end) next = load(blk + 1);
-    const long long at = blk * kBlock + lane * 8;
+  for (; count > 0; --count) {
+    const Block k = Q8 ? next : load(0);
+    if (Q8 && FULL && count > 1) next = load(1);
     float p[8], g[8], m[8], v[8], root[8];
     unpack(k.p, p);
     unpack(k.g, g);
     unpack(k.m, m);
     unpack(k.v, v);
-    // the moments' coefficients take the block's scales along
-    const float cm = Q8 ? h.b1 * k.sm : h.b1, cv = Q8 ? h.b2 * (k.sv * k.sv) : h.b2;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      m[i] = cm * m[i] + h.cg * g[i];
-      v[i] = cv * (Q8 ? v[i] * v[i] : v[i]) + h.cgg * (g[i] * g[i]);
+      if (Q8) {
+        // each operation rounded by itself: a code is a function of the
+        // formula alone, and a run can be followed code by code
+        const float mi = __fmul_rn(m[i], k.sm), ri = __fmul_rn(v[i], k.sv);
+        m[i] = __fadd_rn(__fmul_rn(h.b1, mi), __fmul_rn(h.cg, g[i]));
+        v[i] = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(ri, ri)), __fmul_rn(h.cgg, __fmul_rn(g[i], g[i])));
+      } else {
+        m[i] = h.b1 * m[i] + h.cg * g[i];
+        v[i] = h.b2 * v[i] + h.cgg * (g[i] * g[i]);
+      }
       root[i] = sqrt_fast(v[i]);
       p[i] = p[i] * keep - h.step * (m[i] * rcp_fast(root[i] * h.inv2 + h.eps));
     }
     if (MASTER) {
       Piece<4> o;
       pack(p, o);
-      store_piece<4>(t.master, at, k.n, o);
+      store_piece<4, FULL>(pw, n, o);
     }
-    Piece<PF32 ? 4 : 2> o;
+    Piece<BP> o;
     pack(p, o);
-    store_piece<PF32 ? 4 : 2>(t.p, at, k.n, o);
+    store_piece<BP, FULL>(pp, n, o);
     if constexpr (Q8) {
-      if (k.n < 8) {  // what does not exist has no part in a maximum
+      if (!FULL) {  // what does not exist has no part in a maximum
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i >= k.n) m[i] = root[i] = 0.f;
+          if (i >= n) m[i] = v[i] = root[i] = 0.f;
       }
-      store_codes<false>(t.m, t.m_scale + blk, at, k.n, m);
-      store_codes<true>(t.v, t.v_scale + blk, at, k.n, root);
+      const float2 inv = write_scales(ps, pr, warp_max(m), __fsqrt_rn(warp_max(v)));
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = m[i] * inv.x;
+      store_piece<1, FULL>(pm, n, to_codes(y));
+      store_piece<1, FULL>(pv, n, root_codes(v, root, inv.y));
     } else {
       Piece<4> w;
       pack(m, w);
-      store_piece<4>(t.m, at, k.n, w);
+      store_piece<4, FULL>(pm, n, w);
       pack(v, w);
-      store_piece<4>(t.v, at, k.n, w);
-      if (blk + 1 < end) next = load(blk + 1);
+      store_piece<4, FULL>(pv, n, w);
     }
+    pp += kBlock * BP, pg += kBlock * BG, pm += kBlock * BS, pv += kBlock * BS, ++ps, ++pr;
+    pw += kBlock * (MASTER ? 4 : BP);
   }
+}
+
+// Blocks [blk, end) of one tensor.
+template <bool PF32, bool MASTER, bool GF32, bool Q8>
+__device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamStep& h, long long blk,
+                                            long long end, int lane) {
+  const long long whole = min(end, t.n / kBlock);
+  if (blk < whole) adam_run<PF32, MASTER, GF32, Q8, true>(t, h, blk, static_cast<int>(whole - blk), lane);
+  if (whole < end) adam_run<PF32, MASTER, GF32, Q8, false>(t, h, whole, 1, lane);
 }
 
 template <bool Q8, int CAP>

@@ -561,6 +561,41 @@ def test_adamw_zero_tiny_and_non_finite_blocks():
         assert torch.isnan(u[k][3].float()) and torch.isfinite(torch.cat([u[k][:3], u[k][4:]]).float()).all()
 
 
+def test_adamw_codes_follow_the_formula_bit_for_bit():
+    """8-bit states: codes and scales equal those of the formula with every
+    fp32 operation rounded by itself (what eager elementwise operations do),
+    also at the borders between two codes; two million values a step meet
+    some within an ulp or two of a border."""
+    gen = _gen(7)
+    n = 2_000_000 + 77
+    pad = -(-n // 256) * 256
+    for p, g in ((BF, BF), (F32, F32)):
+        t = _adam_tensor(n, gen, p, g, True)
+        h = sgl.make_adamw_tensors([t])
+
+        def decode(q, s):
+            full = torch.zeros(pad, device="cuda")
+            full[:n] = q.to(F32)
+            return full.view(-1, 256) * s[:, None]
+
+        for step in (1, 2, 3):
+            t["g"].copy_(_randn(n, gen, F32, 1e-3))
+            grad = torch.zeros(pad, device="cuda")
+            grad[:n] = t["g"].to(F32)
+            m, v = decode(t["m"], t["m_scale"]), decode(t["v"], t["v_scale"])
+            grad = grad.view(-1, 256)
+            m = 0.9 * m + (1 - 0.9) * grad
+            v = 0.95 * (v * v) + (1 - 0.95) * (grad * grad)
+            sgl.moe_adamw_step(h, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=step)
+            for key, x in (("m", m), ("v", v.sqrt())):
+                top = x.abs().amax(1, keepdim=True)
+                code = (x * (top.reciprocal() * 448)).to(F8)
+                if key == "v":
+                    code = torch.where((x > 0) & (code.to(F32) == 0), 2.0 ** -9, code.to(F32)).to(F8)
+                assert torch.equal(t[key].view(torch.uint8), code.view(-1)[:n].view(torch.uint8)), (key, step)
+                assert torch.equal(t[key + "_scale"], (top * torch.tensor(1.0 / 448, device="cuda")).view(-1)), (key, step)
+
+
 def test_adamw_update_against_the_definition_over_steps():
     """Twenty steps with fp32 states follow a float64 AdamW of the same
     gradients: errors of 2^-19 of each update add up at most."""
