@@ -288,48 +288,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (leader && elect_one()) {
+      // The tensor pipe holds little more than one instruction, so whatever runs
+      // between two blocks' MMAs shows: descriptors are additions to the stage's
+      // first one, counters stand in for divisions, and the next tile is worked
+      // out under this one's first MMAs.
       constexpr uint32_t major = DIR == kFwd ? 0 : DIR == kDgrad ? kIdescMnA : kIdescMnA | kIdescMnB;
-      int stage = 0, e = 0;
+      constexpr uint64_t step_a = (DIR == kFwd ? 32 : 2048) / 16, step_b = (DIR == kWgrad ? 2048 : 32) / 16;
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + kLinHalf;
+      const uint64_t first_a = DIR == kFwd ? sdesc_k128(a0) : sdesc_mn128(a0, 8192);
+      const uint64_t first_b = DIR == kWgrad ? sdesc_mn128(b0, 8192) : sdesc_k128(b0);
+      uint64_t da = first_a, db = first_b;
+      int stage = 0;
       uint32_t phase = 0, used = 0;  // used: accumulators taken so far
       bool live = true;
+      LinTile t;
+      if (first < tiles) t = tile_at(first, 0);
       for (int i = first; i < tiles && live; i += pairs) {
-        const LinTile t = tile_at(i, e);
-        e = t.e;
+        LinTile next = t;
         const int depth = depth_of(t);
-        if (depth == 0) continue;
+        if (depth == 0) {
+          if (i + pairs < tiles) t = tile_at(i + pairs, t.e);
+          continue;
+        }
         const uint32_t idesc = idesc_bf16(2 * 128, t.n) | major;
         const int chunk = chunk_of(depth);
+        int left = 0;  // contraction left to this accumulator
         uint32_t d = 0;
-        for (int k0 = 0; k0 < depth; k0 += 64) {
-          const bool fresh = k0 % chunk == 0;
+        for (int rest = depth; rest > 0; rest -= 64) {
+          const bool fresh = left <= 0;
           if (fresh) {  // the next accumulator
-            if (k0 > 0) umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
+            if (rest < depth) umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
             const uint32_t buf = used & 1;
             if (!mbar_wait_cluster(&tempty[buf], ((used >> 1) & 1) ^ 1, abort_flag, p.err,
                                    MOE_DEVERR_TIMEOUT)) {
               live = false;
               break;
             }
-            tc_fence_after();
             d = tmem_base + buf * kLinTile;
+            left = chunk;
           }
-          if (!mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+          left -= 64;
+          if (!(DIR == kWgrad  // only there does the other CTA write what this one then reads
+                    ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT)
+                    : mbar_wait(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT))) {
             live = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * kLinStage), b0 = a0 + kLinHalf;
-          const int steps = min(4, (depth - k0 + 15) / 16);
-          for (int k = 0; k < steps; ++k) {
-            const uint64_t da = DIR == kFwd ? sdesc_k128(a0 + k * 32) : sdesc_mn128(a0 + k * 2048, 8192);
-            const uint64_t db = DIR == kWgrad ? sdesc_mn128(b0 + k * 2048, 8192) : sdesc_k128(b0 + k * 32);
-            umma_bf16_pair(d, da, db, idesc, fresh && k == 0 ? 0u : 1u);
+          if (rest > 48) {
+            umma_bf16_pair(d, da, db, idesc, fresh ? 0u : 1u);
+            umma_bf16_pair(d, da + step_a, db + step_b, idesc, 1u);
+            umma_bf16_pair(d, da + 2 * step_a, db + 2 * step_b, idesc, 1u);
+            umma_bf16_pair(d, da + 3 * step_a, db + 3 * step_b, idesc, 1u);
+          } else {
+            for (int k = 0; k < rest; k += 16)
+              umma_bf16_pair(d, da + (k / 16) * step_a, db + (k / 16) * step_b, idesc,
+                             fresh && k == 0 ? 0u : 1u);
           }
           umma_commit_pair_mc(&empty[stage], 0x3);  // frees the stage in both CTAs
-          if (++stage == kLinStages) stage = 0, phase ^= 1;
+          if (rest == depth && i + pairs < tiles) next = tile_at(i + pairs, t.e);
+          da += kLinStage / 16, db += kLinStage / 16;
+          if (++stage == kLinStages) stage = 0, phase ^= 1, da = first_a, db = first_b;
         }
         if (!live) break;
         umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
+        t = next;
       }
     }
     __syncwarp();
