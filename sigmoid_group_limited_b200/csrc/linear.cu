@@ -93,7 +93,7 @@ struct LinParams {
 
 struct LinMaps {
   CUtensorMap a;       // forward: W, 128-row boxes; dgrad: W, wgrad: dy, 64-row boxes
-  CUtensorMap b, b32;  // forward, dgrad: rows, boxes of 128 and of 32; wgrad: x, 64-row boxes
+  CUtensorMap b, b64, b32;  // forward, dgrad: rows, boxes of 128, 64, 32; wgrad: x, 64-row boxes
   CUtensorMap o;       // wgrad: dW, boxes of 32 rows of kLinBoxRow bytes
 };
 
@@ -226,12 +226,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const int depth = depth_of(t), half = t.n / 2;
         const int am = t.m0 + static_cast<int>(rank) * 128;
         const int bc = t.c0 + static_cast<int>(rank) * half;
-        // boxes of B: 32 or 128 rows high (forward, dgrad), 64 features wide (wgrad)
-        const int bbox = DIR == kWgrad ? 64 : half == 128 ? 128 : 32;
-        const int nbox = (half + bbox - 1) / bbox;
-        const uint32_t bytes = kLinHalf + nbox * bbox * 128;
+        // B: 64-feature boxes (wgrad); of rows (forward, dgrad) one box of 128,
+        // or one of 64 and one of 32, or either, the fewest that cover its half
+        const int got = DIR == kWgrad ? (half + 63) & ~63 : half > 96 ? 128 : (half + 31) & ~31;
+        const CUtensorMap* mb = got == 128 ? &m.b : got >= 64 ? &m.b64 : &m.b32;
+        const uint32_t bytes = kLinHalf + got * 128;
         // weights that one tile column reads are not needed again
         const uint64_t pa = DIR != kWgrad && s_off[t.e + 1] - s_off[t.e] <= kLinTile ? pol_w : pol;
+        const int row0 = s_off[t.e];
         for (int k0 = 0; k0 < depth; k0 += 64) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
             live = false;
@@ -240,13 +242,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           uint8_t* sA = smem + stage * kLinStage;
           uint8_t* sB = sA + kLinHalf;
           if (DIR == kWgrad) {
-            const int row = s_off[t.e] + k0;
-            const int rest = depth - k0;
+            const int row = row0 + k0, rest = depth - k0;
             if (rest < 64 && rest % 16 != 0) {  // zeroed before it counts as full
               mbar_arrive_expect_tx(&tail[stage], bytes);
               for (int h = 0; h < 2; ++h)
                 tma_load_2d(sA + h * 8192, &m.a, &tail[stage], am + 64 * h, row, pol);
-              for (int h = 0; h < nbox; ++h)
+              for (int h = 0; h < got / 64; ++h)
                 tma_load_2d(sB + h * 8192, &m.b, &tail[stage], bc + 64 * h, row, pol);
             } else {
               const uint32_t bar = at_leader(&full[stage]);
@@ -256,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               }
               for (int h = 0; h < 2; ++h)
                 tma_load_2d_pair(sA + h * 8192, &m.a, bar, am + 64 * h, row, pol);
-              for (int h = 0; h < nbox; ++h)
+              for (int h = 0; h < got / 64; ++h)
                 tma_load_2d_pair(sB + h * 8192, &m.b, bar, bc + 64 * h, row, pol);
             }
           } else {
@@ -268,9 +269,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               for (int h = 0; h < 2; ++h)
                 tma_load_3d_pair(sA + h * 8192, &m.a, bar, am + 64 * h, k0, t.e, pa);
             }
-            for (int h = 0; h < nbox; ++h)
-              tma_load_2d_pair(sB + h * bbox * 128, bbox == 128 ? &m.b : &m.b32, bar, k0,
-                               bc + h * bbox, pol);
+            tma_load_2d_pair(sB, mb, bar, k0, bc, pol);
+            if (got == 96) tma_load_2d_pair(sB + 8192, &m.b32, bar, k0, bc + 64, pol);
           }
           if (++stage == kLinStages) stage = 0, phase ^= 1;
         }
@@ -621,7 +621,8 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
   } else {
     const int width = dir == kFwd ? d.K : d.N, ld = dir == kFwd ? d.ld_x : d.ld_y;
     ok = map_bf16_blocks(&m.a, b, d.E, d.N, d.K, dir == kFwd ? 128 : 64) &&
-         map_bf16_ld(&m.b, a, d.R, width, ld, 128) && map_bf16_ld(&m.b32, a, d.R, width, ld, 32);
+         map_bf16_ld(&m.b, a, d.R, width, ld, 128) && map_bf16_ld(&m.b64, a, d.R, width, ld, 64) &&
+         map_bf16_ld(&m.b32, a, d.R, width, ld, 32);
   }
   if (!ok) return cudaErrorInvalidValue;
   switch (dir) {
