@@ -159,6 +159,16 @@ def test_grouped_product_many_experts(direction):
     _check(direction, counts, 64, 128, seed=9)
 
 
+@pytest.mark.parametrize("out,accumulate", [(BF, False), (F32, False), (F32, True)])
+@pytest.mark.parametrize("N,K", [(8, 8), (40, 264), (24, 776), (104, 1288), (72, 2568), (8, 7688)])
+def test_few_rows(out, accumulate, N, K):
+    """Up to 128 rows spread over the experts: every unit size (1 to 4 rows of
+    an expert and their remainders), every number of slabs of K."""
+    for counts in ([1], [0, 2], [3, 0, 4, 5, 0, 1], [1, 2, 3, 4, 5, 6, 7, 8, 9] + [0] * 9, [2] * 32 + [1] * 33,
+                   [0] * 30 + [128] + [0], [0] * 31 + [129]):
+        _check("linear", counts, N, K, out=out, accumulate=accumulate, seed=N + K, spare=len(counts) % 2, pad=8)
+
+
 @pytest.mark.parametrize("direction", DIRECTIONS)
 def test_grouped_product_long_depth(direction):
     # 2560 features and a contraction of thousands of rows
@@ -635,3 +645,101 @@ def test_adamw_graph_follows_the_schedule():
         torch.cuda.synchronize()
         for k, x in t.items():
             assert not torch.is_tensor(x) or torch.equal(x.view(torch.uint8), e[k].view(torch.uint8)), k
+
+
+# ------------------------------------------------------------------ together
+def test_expert_layer_forward_backward_and_step():
+    """Routing, permutation, the experts from the separate operators, their
+    gradients and an AdamW step, as a training step runs them: against the
+    fused forward, float64 autograd and differences; then the fused forward
+    on the updated weights."""
+    import workloads
+    from tests.helpers import run_staged, weights
+    cfg = workloads.CONFIGS["tiny"].with_(T=150, limit_routed=3.0)
+    d = workloads.generate(cfg, "cuda:0")
+    T, E, K, H, I = cfg.T, cfg.E, cfg.K, cfg.H, cfg.I
+    R = T * K
+    ws = sgl.alloc_workspace(cfg, T)
+    idx = torch.empty(T, K, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, K, device="cuda")
+    sgl.moe_route(cfg, d["x"], d["Wr"], d["bias"], idx, w, ws)
+
+    def experts_forward():
+        st = run_staged(cfg, d, idx, w)
+        offsets, perm = st["offsets"], st["perm"]
+        x = d["x"][(perm // K).long()]
+        lws = sgl.alloc_linear_workspace(E, R, I, H)
+        gu = torch.empty(R, 2 * I, dtype=BF, device="cuda")
+        g, u = gu[:, :I], gu[:, I:]
+        h = torch.empty(R, I, dtype=BF, device="cuda")
+        y = torch.empty(R, H, device="cuda")
+        sgl.moe_grouped_linear(x, offsets, d["Wg"], g, lws)
+        sgl.moe_grouped_linear(x, offsets, d["Wu"], u, lws)
+        sgl.moe_swiglu(g, u, h, cfg.limit_routed, w=w.view(-1), perm=perm, rows=offsets[E:])
+        sgl.moe_grouped_linear(h, offsets, d["Wd"], y, lws)
+        assert sgl.moe_linear_read_error(lws) == 0
+        # the fused forward keeps gate and up in fp32 and weighs the output: they differ by
+        # the rounding of g, u and the weighted h (2^-8 each) on the way
+        fused = st["y_slot"][perm.long()]
+        assert float((y - fused).norm() / fused.norm()) <= 4 * 2.0 ** -8
+        return x, offsets, perm, lws, g, u, h, y
+
+    x, offsets, perm, lws, g, u, h, y = experts_forward()
+    dy = _randn((R, H), _gen(3), BF)
+    dh, dx = torch.empty_like(h), torch.empty(R, H, device="cuda")
+    dgu = torch.empty(R, 2 * I, dtype=BF, device="cuda")
+    dg, du = dgu[:, :I], dgu[:, I:]
+    dw = torch.empty(R, device="cuda")
+    dW = {k: torch.empty(d[k].shape, device="cuda") for k in ("Wg", "Wu", "Wd")}
+    sgl.moe_grouped_linear_dgrad(dy, offsets, d["Wd"], dh, lws)
+    sgl.moe_grouped_linear_wgrad(dy, h, offsets, dW["Wd"], lws)
+    sgl.moe_swiglu_backward(dh, g, u, dg, du, cfg.limit_routed, w=w.view(-1), perm=perm, dw=dw, rows=offsets[E:])
+    sgl.moe_grouped_linear_dgrad(dg, offsets, d["Wg"], dx, lws)
+    sgl.moe_grouped_linear_dgrad(du, offsets, d["Wu"], dx, lws, accumulate=True)
+    sgl.moe_grouped_linear_wgrad(dg, x, offsets, dW["Wg"], lws)
+    sgl.moe_grouped_linear_wgrad(du, x, offsets, dW["Wu"], lws)
+    assert sgl.moe_linear_read_error(lws) == 0
+
+    ref = {k: d[k].to(F64).requires_grad_() for k in ("Wg", "Wu", "Wd")}
+    xr, wr = x.to(F64).requires_grad_(), w.view(-1).to(F64).requires_grad_()
+    e_of = torch.bucketize(torch.arange(R, device="cuda"), offsets[1:].long(), right=True)
+
+    def loss(W, xx, ww):
+        lim = cfg.limit_routed
+        gg = torch.einsum("rk,rnk->rn", xx, W["Wg"][e_of]).clamp(-lim, lim)
+        uu = torch.einsum("rk,rnk->rn", xx, W["Wu"][e_of]).clamp(-lim, lim)
+        hh = ww[perm.long()][:, None] * torch.nn.functional.silu(gg) * uu
+        return (torch.einsum("rn,rkn->rk", hh, W["Wd"][e_of]) * dy.to(F64)).sum()
+
+    loss(ref, xr, wr).backward()
+    # at most six bf16 roundings lie on a path (g, u, h, dh, dg or du), each 2^-8 of its
+    # tensor's norm at most, passed on by SwiGLU with slopes up to about 1.1 times the weight
+    for name, got, want in ([(k, dW[k], ref[k].grad) for k in dW] + [("x", dx, xr.grad), ("w", dw, wr.grad)]):
+        err = float((got.to(F64) - want).norm() / want.norm())
+        assert err <= 6 * 1.1 * 2.0 ** -8, (name, err)
+    # and against differences of the loss along a direction in every weight
+    with torch.no_grad():
+        dirs = {k: torch.randn(d[k].shape, generator=_gen(11), device="cuda", dtype=F64) * 0.01 for k in dW}
+        t = 1e-3
+        f = [loss({k: ref[k] + s * t * dirs[k] for k in dW}, xr, wr) for s in (1, -1)]
+        diff = float(f[0] - f[1]) / (2 * t)
+        got = sum(float((dW[k].to(F64) * dirs[k]).sum()) for k in dW)
+        scale = math.sqrt(sum(float(ref[k].grad.norm()) ** 2 * 0.01 ** 2 for k in dW))
+        assert abs(got - diff) <= 6 * (6 * 1.1 * 2.0 ** -8) * scale + 0.02 * abs(diff)
+
+    before = {k: d[k].clone() for k in dW}
+    tensors = [dict(p=d[k], g=dW[k], m=torch.zeros(d[k].shape, device="cuda", dtype=F8),
+                    v=torch.zeros(d[k].shape, device="cuda", dtype=F8),
+                    m_scale=torch.zeros(-(-d[k].numel() // 256), device="cuda"),
+                    v_scale=torch.zeros(-(-d[k].numel() // 256), device="cuda")) for k in dW]
+    sgl.moe_adamw_step(sgl.make_adamw_tensors(tensors), lr=1e-2, weight_decay=0.1, step=1)
+    for k in dW:  # first step: each weight with a gradient moves by lr against its sign, then decays
+        moved = d[k].to(F64) - before[k].to(F64) * (1 - 1e-3)
+        clear = dW[k].abs() > 1e-5
+        want = -1e-2 * dW[k].sign().to(F64)
+        tol = 2.0 ** -8 * (before[k].to(F64).abs() + 1e-2) + 1e-2 * 1e-3 + 1e-5
+        assert ((moved - want).abs() <= tol)[clear].all()
+        idle = (offsets[1:] == offsets[:-1]).nonzero()[:, 0]
+        assert (dW[k][idle] == 0).all()
+    experts_forward()
+    assert weights(d) is not None
