@@ -425,34 +425,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           const int wide = kLinBoxRow / (p.out_f32 ? 4 : 2);
 #pragma unroll 1
           for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
+            float v[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            } else {
+              tmem_ld16(tq + c0, v);
+              if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
+            }
             if (elect_one()) bulk_wait_read<0>();  // the warp's box is free again
             __syncwarp();
+            if (!none) tmem_ld_wait();
             auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
               const int at = piece ^ ((lane >> 1) & 3);  // the 64-byte swizzle
               *reinterpret_cast<uint4*>(tile + lane * kLinBoxRow + (at << 4)) = make_uint4(x, y, z, w);
             };
+            if (p.out_f32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 16 columns at a time
-              if (p.out_f32 && h == 1) break;
-              float v[16];
-              if (none) {
+              for (int j = 0; j < 4; ++j)
+                put(j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                    __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+            } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = 0.f;
-              } else {
-                tmem_ld16(tq + c0 + 16 * h, v);
-                tmem_ld_wait();
-              }
-              if (p.out_f32) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  put(4 * h + j, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                      __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-              } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  put(2 * h + j, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-              }
+              for (int j = 0; j < 4; ++j)
+                put(j, pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                    pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
             }
             fence_proxy_async_smem();
             __syncwarp();

@@ -269,6 +269,56 @@ def test_same_bits_streams_and_graphs(direction, counts, N, K):
         assert torch.equal(o, out)
 
 
+@pytest.mark.parametrize("direction", DIRECTIONS)
+def test_fp32_passes_add_in_order(direction):
+    """Depths of several passes, overwriting and accumulating: the same bits
+    every time, while another product keeps the GPU busy on another stream."""
+    counts, N, K = [0, 2500, 3, 900], (264 if direction == "wgrad" else 2000), (2600 if direction == "linear" else 520)
+    a, b, out = _product(direction, counts, N, K, out=F32, seed=8)
+    off, base = _offsets(counts), out.clone()
+    ref, mag = _direct(direction, counts, a, b, out, True)
+    ws = _run(direction, a, b, off, out, True)
+    depth = {"linear": K, "dgrad": N, "wgrad": 2500}[direction]
+    touched = torch.ones_like(out, dtype=torch.bool)
+    if direction == "wgrad":
+        touched[0] = False
+    _check_product(out, ref, mag, depth, touched, True)
+    # the truncation of the tensor core's own sums is bounded by the passes, not by the depth
+    err = float((out.to(F64) - ref)[touched].norm() / ref[touched].norm())
+    assert err <= 768 / 16 * 2.0 ** -24, err
+    side, other = torch.cuda.Stream(), torch.zeros_like(out)
+    for _ in range(3):
+        again = base.clone()
+        torch.cuda.synchronize()
+        _run(direction, a, b, off, other, ws=ws, stream=side)
+        _run(direction, a, b, off, again, True, ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(again, out)
+
+
+def test_addresses_past_32_bits():
+    """Row strides that put the last rows more than 2^31 elements from the first."""
+    R, ld, N, K = 70001, 32768, 16, 24
+    g = _gen(5)
+    big = [torch.empty(R * ld, dtype=BF, device="cuda").view(R, ld) for _ in range(2)]
+    x, y = big[0][:, :K], big[1][:, :N]
+    x.copy_(_randn((R, K), g))
+    W, off = _randn((2, N, K), g), _offsets([R - 300, 300])
+    for direction, a, o in (("linear", x, y), ("dgrad", y, x)):
+        a_in = a.clone()
+        _run(direction, a, W, off, o)
+        ref, mag = _direct(direction, [R - 300, 300], a_in, W, o.clone(), False)
+        _check_product(o.contiguous(), ref, mag, 24, torch.ones_like(ref, dtype=torch.bool))
+    dW = torch.empty(2, N, K, device="cuda")
+    _run("wgrad", y, x, off, dW)
+    ref, mag = _direct("wgrad", [R - 300, 300], y.contiguous(), x.contiguous(), dW, False)
+    _check_product(dW, ref, mag, R, torch.ones_like(dW, dtype=torch.bool))
+    h = big[1][:, 8:8 + K]
+    sgl.moe_swiglu(x, x, h)
+    ref = _swiglu_ref(x, x, 0.0, 1.0)
+    assert ((h.to(F64) - ref).abs() <= (2.0 ** -8 + 2 * FAST) * ref.abs() + 1e-30).all()
+
+
 def test_graph_follows_new_offsets():
     """A captured product reads the offsets when it runs: another split of the
     rows needs no new capture."""
@@ -544,6 +594,28 @@ def test_adamw_neighbours_keep_their_values():
         for k, buf in bufs.items():
             pad = 4 if k.endswith("_scale") else 32
             assert (buf[:pad].float() == 1).all() and (buf[-pad:].float() == 1).all(), k
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_adamw_past_32_bits(q8):
+    """A tensor of more than 2^31 elements: its end moves as the same values do alone."""
+    n, tail = 2 ** 31 + 700, 4096 + 700 % 256
+    gen = _gen(8)
+    small = _adam_tensor(tail, gen, BF, BF, q8)
+    lo = n - tail
+    assert lo % 256 == 0
+    t = {}
+    for k, x in small.items():
+        if torch.is_tensor(x):
+            scale = k.endswith("_scale")
+            t[k] = torch.zeros(-(-n // 256) if scale else n, dtype=x.dtype, device="cuda")
+            t[k].view(torch.uint8)[-x.numel() * x.element_size():] = x.view(torch.uint8)
+    _step([t])
+    _step([small])
+    for k, x in small.items():
+        if torch.is_tensor(x):
+            assert torch.equal(t[k].view(torch.uint8)[-x.numel() * x.element_size():], x.view(torch.uint8)), k
+    assert not t["p"][:lo:4097].any()
 
 
 def test_adamw_zero_tiny_and_non_finite_blocks():
