@@ -397,45 +397,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
     int e = 0;
     uint32_t used = 0;
+    const int wide = kLinBoxRow / (p.out_f32 ? 4 : 2);  // columns of a box
     for (int i = first; i < tiles; i += pairs) {
       const LinTile t = tile_at(i, e);
       e = t.e;
       const int f0 = t.m0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's features on M
       const int depth = depth_of(t);
-      const bool none = depth == 0;
+      if (DIR == kWgrad && depth == 0) {
+        // an expert without rows: this CTA's share of its matrix, which is one
+        // stretch of memory, whatever the tile (tile by tile, the narrow ones at
+        // its edges made this up to a third slower than writing products)
+        if (p.accumulate) continue;
+        const long long all = static_cast<long long>(p.M) * p.C * (p.out_f32 ? 4 : 2) / 16;
+        const int shares = 2 * p.mt * p.ct;
+        const int share = 2 * (t.c0 / kLinTile * p.mt + t.m0 / kLinTile) + static_cast<int>(rank);
+        uint4* o = static_cast<uint4*>(p.out) + t.e * all;
+        const long long end = all * (share + 1) / shares;
+        for (long long j = all * share / shares + (tid - kLinEpiWarp0 * 32); j < end; j += kLinEpiWarps * 32)
+          o[j] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
       const int chunk = chunk_of(depth);
-      if (none && p.accumulate) continue;
       bool live = true;
       for (int k0 = 0; k0 == 0 || k0 < depth; k0 += chunk) {
         const bool add = p.accumulate || k0 > 0;
         const uint32_t buf = used & 1;
-        if (!none) {
-          if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
-            live = false;
-            break;
-          }
-          tc_fence_after();
+        if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+          live = false;
+          break;
         }
+        tc_fence_after();
         // the pass before has reached the output (bulk stores keep no order)
         if (DIR == kWgrad && k0 > 0 && elect_one()) bulk_wait<0>();
         const uint32_t tq = tmem_base + buf * kLinTile + (static_cast<uint32_t>(q * 32) << 16);
         if (DIR == kWgrad) {
           // lane = row of D, whose columns are adjacent in dW: boxes of 32 rows
           // by TMA. The box ends at dW's edges by itself.
-          const int wide = kLinBoxRow / (p.out_f32 ? 4 : 2);
 #pragma unroll 1
           for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
             float v[32];
-            if (none) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            } else {
-              tmem_ld16(tq + c0, v);
-              if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
-            }
+            tmem_ld16(tq + c0, v);
+            if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
             if (elect_one()) bulk_wait_read<0>();  // the warp's box is free again
             __syncwarp();
-            if (!none) tmem_ld_wait();
+            tmem_ld_wait();
             auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
               const int at = piece ^ ((lane >> 1) & 3);  // the 64-byte swizzle
               *reinterpret_cast<uint4*>(tile + lane * kLinBoxRow + (at << 4)) = make_uint4(x, y, z, w);
@@ -515,17 +520,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             }
           }
         }
-        if (!none) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            // hands over tensor memory only, which the tcgen05 fence orders; a release
-            // at cluster scope would wait for this tile's global stores
-            if (leader) mbar_arrive(&tempty[buf]);
-            else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
-          }
-          ++used;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          // hands over tensor memory only, which the tcgen05 fence orders; a release
+          // at cluster scope would wait for this tile's global stores
+          if (leader) mbar_arrive(&tempty[buf]);
+          else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
         }
+        ++used;
       }
       if (!live) break;
     }
