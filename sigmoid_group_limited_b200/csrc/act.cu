@@ -7,8 +7,10 @@
 //   du = w dh a s                 where |u| <= limit, else 0
 //   dw = sum_i dh a s b
 //
-// Both are bound by HBM: 6 bytes per element forward (g, u in, h out), 10
-// backward. A group of G lanes owns a row (so dw is one shuffle reduction,
+// Both are bound by memory: 6 bytes per element forward (g, u in, h out), 10
+// backward; 32768 x 768 take 28.5 us (5.3 TB/s) and 48 us (5.1 TB/s), launch
+// included. Fewer or more pieces under way per lane, two to six blocks an SM
+// and the next row's weight loaded ahead change that by less than 5 %. A group of G lanes owns a row (so dw is one shuffle reduction,
 // in a fixed order) and moves 8 features (16 bytes) per lane and tensor.
 // Everything between the loads and the one rounding of each output is fp32;
 // the exponential is the hardware one (a few ulp, far below bf16's half ulp).

@@ -9,7 +9,9 @@
 // warp reduction and nothing is read twice. No atomics: an element is owned
 // by one lane. The arithmetic of 8-bit states fills most of the issue slots, so
 // it is kept short: roots and reciprocals are the hardware's wherever they do
-// not decide a code.
+// not decide a code. 144 M elements with fp32 states: 668 us, 6.0 TB/s; 377 M
+// with 8-bit states: 766 us sustained, 690 us in short runs, 5.0 to 5.5 TB/s at
+// 57 instructions an element and 0.84 of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -27,7 +29,8 @@ constexpr int kBlock = MOE_STATE_BLOCK;  // 32 lanes x 8 elements
 // Most blocks a warp takes at a time. Starting on a tensor (its pointers, the
 // first loads with nothing to compute meanwhile) costs about as much as a few
 // blocks: 8-bit states over 377 M elements took 989, 893, 708 and 732 us with
-// 1, 8, 32 and 64. Fewer where warps would be left without work.
+// 1, 8, 32 and 64 in the form they were chosen with. Fewer where warps would be
+// left without work.
 constexpr int kSpan = 32;
 // Tensors per launch: a parameter block of 3 KB, or of 26 KB for longer lists
 // (240 small tensors: 11.6 us in one launch, 22 us in launches of 40).

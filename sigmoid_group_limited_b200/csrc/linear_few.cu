@@ -12,6 +12,10 @@
 // fp32, each lane over its pieces of K in order, then a butterfly over the
 // lanes: the same bits every time.
 //
+// Bound by HBM from some 32 rows on: 128 rows of 512 experts, 100 of them
+// touched, 768 x 2560 weights, 75 us = 5.3 TB/s; a token's 8 rows (31 MB) take
+// about 9 us, most of it launch, the offsets' latency and one round of loads.
+//
 // A unit is named by its first row: the blocks fill a table [R] with the
 // expert and the row count at every row that starts a unit, from one pass over
 // the offsets, and need no prefix sum.
