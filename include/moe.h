@@ -292,8 +292,9 @@ MOE_API size_t moe_linear_workspace_size(const moe_linear_desc* desc);
 
 /* Forward: y[r,:N] (+)= x[r,:K] W_e^T for every row r of every expert e.
  * x [R, ld_x] bf16, offsets [E+1] int32, W [E,N,K] bf16; out: y [R, ld_y].
- * fp32 accumulation over K, one rounding at the end. Each call's result is
- * the same bits every time. Offsets that do not ascend within [0, R] set
+ * fp32 accumulation over K, one rounding at the end (additions to an fp32
+ * output may flush subnormals). Each call's result is the same bits every
+ * time. offsets[0] may be above 0: rows below it are spare, too. Offsets that do not ascend within [0, R] set
  * MOE_DEVERR_OFFSETS, and nothing is computed. */
 MOE_API moe_status moe_grouped_linear(const moe_linear_desc* desc, const void* x,
                                       const int32_t* offsets, const void* W, void* y, void* ws,

@@ -38,7 +38,7 @@
 // towards zero: about 1.7e-8 of the sum per 16-deep step, 6e-6 at a depth of
 // 6000. A bf16 result does not see it. An fp32 result is made in passes of at
 // most 768: each pass starts a fresh accumulator and the epilogue adds it to the
-// output in fp32 (rounded to nearest), which holds the error at about 8e-7 at
+// output in fp32 (rounded to nearest, subnormals flushed), which holds the error at about 8e-7 at
 // any depth. The adds are reductions in L2 (one per element and pass, by the
 // same thread in order, so the result is the same every time).
 //
@@ -441,6 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           live = false;
           break;
         }
+        __syncwarp();  // tensor-memory reads are warp-wide
         tc_fence_after();
         // the pass before has reached the output (bulk stores keep no order)
         if (DIR == kWgrad && k0 > 0 && elect_one()) bulk_wait<0>();

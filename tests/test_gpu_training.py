@@ -176,6 +176,29 @@ def test_grouped_product_long_depth(direction):
 
 
 @pytest.mark.parametrize("direction", DIRECTIONS)
+@pytest.mark.parametrize("counts", [[3, 0, 2], [40, 0, 150, 9]], ids=["few", "many"])
+def test_spare_rows_in_front(direction, counts):
+    """offsets[0] above zero: the rows before the first expert are spare."""
+    lead, N, K = 21, 72, 136
+    a, b, out = _product(direction, [lead] + counts, N, K, seed=7)
+    off = _offsets([lead] + counts)[1:].clone()
+    a[:lead] = float("nan")
+    if direction == "wgrad":
+        b[:lead] = float("nan")
+        out = out[1:].contiguous()
+    else:
+        b = b[1:].contiguous()
+        out[:lead] = 3.0
+    ref, mag = _direct(direction, counts, a[lead:], b[lead:] if direction == "wgrad" else b,
+                       out if direction == "wgrad" else out[lead:], False)
+    ws = _run(direction, a, b, off, out)
+    assert sgl.moe_linear_read_error(ws) == 0
+    got = out if direction == "wgrad" else out[lead:]
+    _check_product(got, ref, mag, 200, torch.ones_like(got, dtype=torch.bool))
+    assert direction == "wgrad" or (out[:lead] == 3.0).all()
+
+
+@pytest.mark.parametrize("direction", DIRECTIONS)
 def test_no_rows_at_all(direction):
     counts, N, K = [0, 0, 0], 16, 24
     for spare in (0, 5):
