@@ -94,6 +94,10 @@ def _current_stream(dev: int) -> int:
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
+# the current device's index, without torch.cuda's initialisation check (the tensors exist)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call(fn, where: str, tensors, stream, *args) -> None:
     """fn(*args, stream) on the tensors' device; None among them is skipped."""
     dev = tensors[0].get_device()
@@ -106,7 +110,7 @@ def _call(fn, where: str, tensors, stream, *args) -> None:
         s = _current_stream(dev)
     else:
         s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             st = fn(*args, s)
     else:
@@ -209,29 +213,38 @@ def moe_linear_read_error(ws, stream=None) -> int:
 
 
 # ------------------------------------------------------------------ SwiGLU
+def _like(t, name: str, shape, stride) -> int:
+    """The row stride of t, which must have g's shape and type."""
+    if t.dtype is torch.bfloat16 and t.shape == shape:
+        if t.stride() == stride:
+            return stride[0] if shape[0] > 1 else shape[1]
+        return _rows(t, name)[2]
+    _rows(t, name)
+    raise ValueError(f"{name}: expected the shape of g, {tuple(shape)}")
+
+
 def _swiglu_desc(g, u, h, limit: float, h_name: str, dg=None, du=None):
     R, I, ld_g = _rows(g, "g")
-    ur, ui, ld_u = _rows(u, "u")
-    hr, hi, ld_h = _rows(h, h_name)
-    if (ur, ui) != (R, I) or (hr, hi) != (R, I) or ld_u != ld_g:
-        raise ValueError(f"g, u and {h_name} must have one shape, g and u one row stride")
-    ld_dg = ld_g
+    shape, stride = g.shape, g.stride()
+    if _like(u, "u", shape, stride) != ld_g:
+        raise ValueError("g and u must have one row stride")
+    ld_h, ld_dg = _like(h, h_name, shape, stride), ld_g
     if dg is not None:
-        a, b = _rows(dg, "dg"), _rows(du, "du")
-        if a != b or a[:2] != (R, I):
-            raise ValueError("dg and du must have the shape of g and one row stride")
-        ld_dg = a[2]
-    return moe_swiglu_desc(R, I, ld_g, ld_h, ld_dg, float(limit))
+        ld_dg = _like(dg, "dg", shape, stride)
+        if _like(du, "du", shape, stride) != ld_dg:
+            raise ValueError("dg and du must have one row stride")
+    return moe_swiglu_desc(R, I, ld_g, ld_h, ld_dg, limit)
 
 
 def _weight_args(d, w, perm, rows):
-    n_w = 0 if w is None else w.numel()
-    if w is None and perm is not None:
-        raise ValueError("perm without w")
+    rp = None if rows is None else _flat(rows, "rows", torch.int32, 1, True)
+    if w is None:
+        if perm is not None:
+            raise ValueError("perm without w")
+        return None, None, 0, rp
     if perm is None:
-        _flat(w, "w", torch.float32, d.R, True)
-    return (_flat(w, "w", torch.float32), _flat(perm, "perm", torch.int32, d.R, True), n_w,
-            _flat(rows, "rows", torch.int32, 1, True))
+        return _flat(w, "w", torch.float32, d.R, True), None, 0, rp
+    return _flat(w, "w", torch.float32), _flat(perm, "perm", torch.int32, d.R, True), w.numel(), rp
 
 
 def moe_swiglu(g, u, h, limit: float = 0.0, w=None, perm=None, rows=None, stream=None) -> None:
@@ -250,7 +263,7 @@ def moe_swiglu_backward(dh, g, u, dg, du, limit: float = 0.0, w=None, perm=None,
     with w, dw (fp32, laid out like w; optional)."""
     d = _swiglu_desc(g, u, dh, limit, "dh", dg, du)
     wp, pp, n_w, rp = _weight_args(d, w, perm, rows)
-    if dw is not None and (w is None or dw.numel() != n_w):
+    if dw is not None and (w is None or dw.numel() != w.numel()):
         raise ValueError("dw: needs w and its size")
     _call(lib().moe_swiglu_backward, "moe_swiglu_backward", (dh, g, u, dg, du, w, perm, rows, dw), stream,
           ctypes.byref(d), dh.data_ptr(), g.data_ptr(), u.data_ptr(), wp, pp, n_w, rp, dg.data_ptr(),
