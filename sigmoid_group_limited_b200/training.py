@@ -283,27 +283,35 @@ def make_adamw_tensors(tensors: Sequence[dict]) -> AdamWTensors:
     p (bf16 or fp32, contiguous), g (bf16 or fp32), m and v (both fp32, or
     both float8_e4m3fn with m_scale and v_scale, one fp32 per MOE_STATE_BLOCK
     elements), optionally master (fp32, with a bf16 p) and wd_scale."""
-    out, keep = (moe_adamw_tensor * max(1, len(tensors)))(), []
-    for i, t in enumerate(tensors):
+    out, keep, dev = (moe_adamw_tensor * max(1, len(tensors)))(), [], None
+    f32 = torch.float32
+    for o, t in zip(out, tensors):
         p, g, m, v = t["p"], t["g"], t["m"], t["v"]
-        n = p.numel()
-        if m.dtype not in _STATES or v.dtype != m.dtype:
-            raise ValueError("m and v: expected both float32 or both float8_e4m3fn")
-        q8 = m.dtype == torch.float8_e4m3fn
         master, ms, vs = t.get("master"), t.get("m_scale"), t.get("v_scale")
+        n, state = p.numel(), m.dtype
+        if state not in _STATES or v.dtype is not state:
+            raise ValueError("m and v: expected both float32 or both float8_e4m3fn")
+        q8 = state is not f32
         if q8 != (ms is not None) or q8 != (vs is not None):
             raise ValueError("8-bit states, and only they, have m_scale and v_scale")
-        blocks = -(-n // MOE_STATE_BLOCK)
-        out[i] = moe_adamw_tensor(
-            _flat(p, "p", p.dtype), _flat(master, "master", torch.float32, n), _flat(g, "g", g.dtype, n),
-            _flat(m, "m", m.dtype, n), _flat(v, "v", v.dtype, n), _flat(ms, "m_scale", torch.float32, blocks),
-            _flat(vs, "v_scale", torch.float32, blocks), n, _out_type(p, "p"), _out_type(g, "g"),
-            _STATES[m.dtype], float(t.get("wd_scale", 1.0)))
-        mine = [x for x in (p, g, m, v, master, ms, vs) if x is not None]
-        if any(not x.is_cuda or x.device != p.device for x in mine):
-            raise ValueError("expected CUDA tensors of one device")
-        if keep and keep[0].device != p.device:
-            raise ValueError("the tensors lie on different devices")
+        o.p, o.g = _flat(p, "p", p.dtype), _flat(g, "g", g.dtype, n)
+        o.m, o.v = _flat(m, "m", state, n), _flat(v, "v", state, n)
+        o.n, o.state_type, o.wd_scale = n, _STATES[state], t.get("wd_scale", 1.0)
+        o.p_type, o.g_type = _out_type(p, "p"), _out_type(g, "g")
+        mine = [p, g, m, v]
+        if master is not None:
+            o.master = _flat(master, "master", f32, n)
+            mine.append(master)
+        if q8:
+            blocks = -(-n // MOE_STATE_BLOCK)
+            o.m_scale = _flat(ms, "m_scale", f32, blocks)
+            o.v_scale = _flat(vs, "v_scale", f32, blocks)
+            mine += (ms, vs)
+        for x in mine:
+            d = x.get_device()
+            if d < 0 or (dev is not None and d != dev):
+                raise ValueError("expected CUDA tensors of one device")
+            dev = d
         keep += mine
     return AdamWTensors(out, len(tensors), keep)
 
