@@ -7,7 +7,8 @@
 //   wgrad    dW[e,n,k] = sum_r dy[r,n] x[r,k]
 //
 // One kernel, three sets of operands. A pair of CTAs (a cluster of two) owns
-// an output tile D[256][up to 256]: M = 256 MMAs, each CTA with 128 rows of A
+// an output tile D[256][up to 256] (128 columns where few tiles would leave
+// pairs idle): M = 256 MMAs, each CTA with 128 rows of A
 // and half of B's columns in its shared memory and 128 rows of D in its
 // tensor memory. Forward and dgrad put the features (regular, hundreds) on M
 // and an expert's rows (ragged) on N, so a short tile costs a narrower MMA,
@@ -98,7 +99,7 @@ struct LinParams {
   int E, R;
   int M, C;        // features on M; on N (wgrad only)
   int depth;       // contraction length (forward, dgrad)
-  int mt, ct;      // feature tiles on M; on N (wgrad only)
+  int mt;          // feature tiles on M
   long long ld;    // output row stride
   int out_f32, accumulate;
   const int32_t* offsets;
@@ -146,7 +147,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* bad = const_cast<int*>(abort_flag) + 1;
-  static_assert(8 * (3 * kLinStages + 4) + 12 <= kLinCtrl, "ctrl");
+  int* count = bad + 1;  // [2] column tiles of 256 and of 128
+  static_assert(8 * (3 * kLinStages + 4) + 20 <= kLinCtrl, "ctrl");
   int* s_off = reinterpret_cast<int*>(ctrl + kLinCtrl);  // [E+1] row offsets
   int* s_tile = s_off + p.E + 1;                         // [E+1] tiles before expert e
   int* wsum = s_tile + p.E + 1;                          // [33]
@@ -167,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       mbar_init(&tempty[a], 2 * kLinEpiWarps);  // the epilogue warps of both CTAs
     }
     *abort_flag = 0;
-    *bad = 0;
+    *bad = count[0] = count[1] = 0;
     fence_mbar_init();
     if (p.R > 0) {
       prefetch_tmap(&m.a);
@@ -182,22 +184,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   for (int i = tid; i <= p.E; i += kLinThreads) s_off[i] = p.offsets[i];
   tc_fence_before();
   __syncthreads();
+  const int first = blockIdx.x / 2, pairs = gridDim.x / 2;
+  int n256 = 0, n128 = 0;  // column tiles of this thread's experts
   for (int e = tid; e <= p.E; e += kLinThreads) {
     const int lo = s_off[e], hi = e < p.E ? s_off[e + 1] : p.R;
-    if (lo < 0 || hi < lo || hi > p.R) *bad = 1;
-    s_tile[e] = e == p.E ? 0
-                : DIR == kWgrad ? p.mt * p.ct
-                                : p.mt * ((hi - lo + kLinTile - 1) / kLinTile);
+    if (lo < 0 || hi < lo || hi > p.R) {
+      *bad = 1;
+    } else if (e < p.E) {
+      const int cols = DIR == kWgrad ? p.C : hi - lo;
+      n256 += (cols + kLinTile - 1) / kLinTile;
+      n128 += (cols + kLinTile / 2 - 1) / (kLinTile / 2);
+    }
   }
+  atomicAdd(&count[0], n256);
+  atomicAdd(&count[1], n128);
   __syncthreads();
   const bool go = *bad == 0;  // the same in every CTA: all read the same offsets
   if (!go && tid == 0) atomicExch(p.err, MOE_DEVERR_OFFSETS);
+  // Columns of a tile: 256, or 128 where so few tiles leave pairs idle in the
+  // last of at most three rounds and the halves fill them (input gradient of 5003
+  // rows, 32 experts of 200 x 1000: 21 us with 256, 17 with 128; weight gradient
+  // of a single 768 x 2560 expert, 4096 rows: 28 and 22; 8 experts: 22 and 22).
+  const int r256 = (count[0] * p.mt + pairs - 1) / pairs, r128 = (count[1] * p.mt + pairs - 1) / pairs;
+  const int wide = r256 <= 3 && r128 < 2 * r256 ? kLinTile / 2 : kLinTile;
+  const int ct = DIR == kWgrad ? (p.C + wide - 1) / wide : 0;  // column tiles of an expert
+  if (go)
+    for (int e = tid; e <= p.E; e += kLinThreads)
+      s_tile[e] = e == p.E ? 0
+                           : p.mt * (DIR == kWgrad ? ct : (s_off[e + 1] - s_off[e] + wide - 1) / wide);
+  __syncthreads();
   if (go) smem_exscan(s_tile, p.E + 1, wsum);
   cluster_sync();  // both CTAs' barriers exist before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int tiles = go ? s_tile[p.E] : 0;
-  const int first = blockIdx.x / 2, pairs = gridDim.x / 2;
   auto at_leader = [&](uint64_t* bar) { return mapa_shared(smem_u32(bar), 0); };
 
   // Tile i; e: the expert of the caller's previous tile (tiles ascend).
@@ -208,14 +228,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const int rows = s_off[e + 1] - s_off[e];
     t.e = e;
     t.m0 = (local % p.mt) * kLinTile;
-    const int c = (local / p.mt) * kLinTile;
+    const int c = (local / p.mt) * wide;
     if (DIR == kWgrad) {
       t.c0 = c;
       t.rows = rows;
-      t.cols = min(kLinTile, p.C - c);
+      t.cols = min(wide, p.C - c);
     } else {
       t.c0 = s_off[e] + c;
-      t.cols = t.rows = min(kLinTile, rows - c);
+      t.cols = t.rows = min(wide, rows - c);
     }
     t.n = (t.cols + 31) & ~31;
     return t;
@@ -247,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const CUtensorMap* mb = got == 128 ? &m.b : got >= 64 ? &m.b64 : &m.b32;
         const uint32_t bytes = kLinHalf + got * 128;
         // weights that one tile column reads are not needed again
-        const uint64_t pa = DIR != kWgrad && s_off[t.e + 1] - s_off[t.e] <= kLinTile ? pol_w : pol;
+        const uint64_t pa = DIR != kWgrad && s_off[t.e + 1] - s_off[t.e] <= wide ? pol_w : pol;
         const int row0 = s_off[t.e];
         for (int k0 = 0; k0 < depth; k0 += 64) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
@@ -412,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
     int e = 0;
     uint32_t used = 0;
-    const int wide = kLinBoxRow / (p.out_f32 ? 4 : 2);  // columns of a box
+    const int box = kLinBoxRow / (p.out_f32 ? 4 : 2);  // columns of a stored box
     for (int i = first; i < tiles; i += pairs) {
       const LinTile t = tile_at(i, e);
       e = t.e;
@@ -424,8 +444,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         // its edges made this up to a third slower than writing products)
         if (p.accumulate) continue;
         const long long all = static_cast<long long>(p.M) * p.C * (p.out_f32 ? 4 : 2) / 16;
-        const int shares = 2 * p.mt * p.ct;
-        const int share = 2 * (t.c0 / kLinTile * p.mt + t.m0 / kLinTile) + static_cast<int>(rank);
+        const int shares = 2 * p.mt * ct;
+        const int share = 2 * (t.c0 / wide * p.mt + t.m0 / kLinTile) + static_cast<int>(rank);
         uint4* o = static_cast<uint4*>(p.out) + t.e * all;
         const long long end = all * (share + 1) / shares;
         for (long long j = all * share / shares + (tid - kLinEpiWarp0 * 32); j < end; j += kLinEpiWarps * 32)
@@ -450,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           // lane = row of D, whose columns are adjacent in dW: boxes of 32 rows
           // by TMA. The box ends at dW's edges by itself.
 #pragma unroll 1
-          for (int c0 = wide * part; c0 < t.cols && f0 < p.M; c0 += 2 * wide) {
+          for (int c0 = box * part; c0 < t.cols && f0 < p.M; c0 += 2 * box) {
             float v[32];
             tmem_ld16(tq + c0, v);
             if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
@@ -593,8 +613,9 @@ cudaError_t run(const moe_linear_desc& d, LinParams p, const LinMaps& m, cudaStr
   int pairs = 0;
   if ((e = resident_pairs<DIR>(kLinSmem, &pairs)) != cudaSuccess) return e;
   // no more pairs than tiles there can be
-  const long long most = DIR == kWgrad ? 1LL * d.E * p.mt * p.ct
-                                       : 1LL * p.mt * (cdiv(d.R, kLinTile) + (d.E < d.R ? d.E : d.R));
+  const long long most = DIR == kWgrad
+                             ? 1LL * d.E * p.mt * cdiv(p.C, kLinTile / 2)
+                             : 1LL * p.mt * (cdiv(d.R, kLinTile / 2) + (d.E < d.R ? d.E : d.R));
   if (most < pairs) pairs = static_cast<int>(most);
   return launch_pdl(grouped_linear<DIR>, dim3(2 * pairs), dim3(kLinThreads), kLinSmem, s, p, m);
 }
@@ -619,7 +640,6 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
   p.C = dir == kWgrad ? d.K : 0;
   p.depth = dir == kFwd ? d.K : d.N;
   p.mt = cdiv(p.M, kLinTile);
-  p.ct = cdiv(p.C, kLinTile);
   p.ld = dir == kFwd ? d.ld_y : dir == kDgrad ? d.ld_x : d.K;
   p.out_f32 = d.out_type == MOE_T_F32;
   p.accumulate = d.accumulate != 0;
