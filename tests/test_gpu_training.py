@@ -159,6 +159,16 @@ def test_grouped_product_many_experts(direction):
     _check(direction, counts, 64, 128, seed=9)
 
 
+@pytest.mark.parametrize("direction", DIRECTIONS)
+@pytest.mark.parametrize("out", [BF, F32])
+def test_grouped_product_many_wide_tiles(direction, out):
+    """Enough work for full-width tiles (narrower ones serve small calls): rows
+    around the multiples of 256, several rounds per pair."""
+    counts = [(e * 97) % 530 for e in range(56)] + [0, 255, 256, 257, 511, 512, 513, 1]
+    n, k = (72, 776) if direction == "dgrad" else (776, 328)
+    _check(direction, counts, n, k, out=out, seed=13, spare=33)
+
+
 @pytest.mark.parametrize("out,accumulate", [(BF, False), (F32, False), (F32, True)])
 @pytest.mark.parametrize("N,K", [(8, 8), (40, 264), (24, 776), (104, 1288), (72, 2568), (8, 7688)])
 def test_few_rows(out, accumulate, N, K):
