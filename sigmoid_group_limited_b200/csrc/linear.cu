@@ -476,7 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
             if (elect_one()) bulk_wait_read<0>();  // the warp's box is free again
             __syncwarp();
-            tmem_ld_wait();
+            tmem_ld_wait_for<16>(v);
+            if (!p.out_f32) tmem_ld_wait_for<16>(v + 16);
             auto put = [&](int piece, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
               const int at = piece ^ ((lane >> 1) & 3);  // the 64-byte swizzle
               *reinterpret_cast<uint4*>(tile + lane * kLinBoxRow + (at << 4)) = make_uint4(x, y, z, w);
@@ -507,14 +508,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             if (!p.out_f32) {
               // 32 features x 32 token rows, read as 8 x 8 fragments and stored
               // transposed: rows of 32 features
-              float v[2][16];
-              tmem_ld_16x32(tq + c0, v[0]);
-              tmem_ld_16x32(tq + (16u << 16) + c0, v[1]);
-              tmem_ld_wait();
+              float v[32];
+              tmem_ld_16x32(tq + c0, v);
+              tmem_ld_16x32(tq + (16u << 16) + c0, v + 16);
+              tmem_ld_wait_for<32>(v);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint32_t r[4] = {pack_bf16(v[0][4 * j], v[0][4 * j + 1]), pack_bf16(v[0][4 * j + 2], v[0][4 * j + 3]),
-                                       pack_bf16(v[1][4 * j], v[1][4 * j + 1]), pack_bf16(v[1][4 * j + 2], v[1][4 * j + 3])};
+                const float *lo = v + 4 * j, *hi = v + 16 + 4 * j;
+                const uint32_t r[4] = {pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]),
+                                       pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
                 stmatrix4_trans(tile + (8 * j + (lane & 7)) * kLinPitch + (lane >> 3) * 16, r);
               }
               __syncwarp();
@@ -533,7 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
               float v[32];
               tmem_ld16(tq + c0, v);
               tmem_ld16(tq + c0 + 16, v + 16);
-              tmem_ld_wait();
+              tmem_ld_wait_for<32>(v);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
 #pragma unroll

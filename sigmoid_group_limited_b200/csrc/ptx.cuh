@@ -405,6 +405,14 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float* v) {
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+// The same for the N values that the loads deliver: no use of them can be
+// scheduled before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(float* v) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
 
 // Shared-memory matrix descriptor for a K-major bf16 tile stored as rows of
 // 128 bytes (64 elements) with the 128-byte swizzle, 8-row groups 1024 bytes
