@@ -228,7 +228,7 @@ __device__ __forceinline__ Piece<1> root_codes(const float* v, const float* root
 struct AdamStep {
   float lr, step, inv2;  // rate, rate / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   float b1, b2, eps;
-  float cg, cgg;         // (1 - beta1) and (1 - beta2) with the gradient scale and its square
+  float b1c, b2c, gs;    // 1 - beta1, 1 - beta2, gradient scale
 };
 
 // `count` blocks of one tensor from blk on, all of them whole (FULL) or the one
@@ -272,17 +272,23 @@ __device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamStep& h,
     unpack(k.g, g);
     unpack(k.m, m);
     unpack(k.v, v);
+    // The gradient is scaled before it is squared: under a scale that brings it
+    // back into range neither g^2 nor the scale's square need fit fp32. (8-bit
+    // states, 377 M elements: 766 us with this product, 759 without; a branch around
+    // it for a scale of one: 764.)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(h.gs, g[i]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (Q8) {
         // each operation rounded by itself: a code is a function of the
         // formula alone, and a run can be followed code by code
         const float mi = __fmul_rn(m[i], k.sm), ri = __fmul_rn(v[i], k.sv);
-        m[i] = __fadd_rn(__fmul_rn(h.b1, mi), __fmul_rn(h.cg, g[i]));
-        v[i] = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(ri, ri)), __fmul_rn(h.cgg, __fmul_rn(g[i], g[i])));
+        m[i] = __fadd_rn(__fmul_rn(h.b1, mi), __fmul_rn(h.b1c, g[i]));
+        v[i] = __fadd_rn(__fmul_rn(h.b2, __fmul_rn(ri, ri)), __fmul_rn(h.b2c, __fmul_rn(g[i], g[i])));
       } else {
-        m[i] = h.b1 * m[i] + h.cg * g[i];
-        v[i] = h.b2 * v[i] + h.cgg * (g[i] * g[i]);
+        m[i] = h.b1 * m[i] + h.b1c * g[i];
+        v[i] = h.b2 * v[i] + h.b2c * (g[i] * g[i]);
       }
       root[i] = sqrt_fast(v[i]);
       p[i] = p[i] * keep - h.step * (m[i] * rcp_fast(root[i] * h.inv2 + h.eps));
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas)
   pdl_wait();
   float lr = P.lr, c1 = P.c1, rc2 = P.rc2, gs = P.gs;
   if (P.dyn != nullptr) lr = P.dyn[0], c1 = P.dyn[1], rc2 = P.dyn[2], gs = P.dyn[3];
-  const AdamStep h = {lr, lr / c1, 1.f / rc2, P.b1, P.b2, P.eps, P.b1c * gs, P.b2c * gs * gs};
+  const AdamStep h = {lr, lr / c1, 1.f / rc2, P.b1, P.b2, P.eps, P.b1c, P.b2c, gs};
   const int lane = threadIdx.x & 31;
   const long long total = P.first[P.count];
   const long long warps = static_cast<long long>(gridDim.x) * (kAdamThreads / 32);
