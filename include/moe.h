@@ -292,10 +292,17 @@ MOE_API size_t moe_linear_workspace_size(const moe_linear_desc* desc);
 
 /* Forward: y[r,:N] (+)= x[r,:K] W_e^T for every row r of every expert e.
  * x [R, ld_x] bf16, offsets [E+1] int32, W [E,N,K] bf16; out: y [R, ld_y].
- * fp32 accumulation over K, one rounding at the end (additions to an fp32
- * output may flush subnormals). Each call's result is the same bits every
- * time. offsets[0] may be above 0: rows below it are spare, too. Offsets that do not ascend within [0, R] set
- * MOE_DEVERR_OFFSETS, and nothing is computed. */
+ * Sums are fp32. The tensor core cuts its sums instead of rounding them, so it
+ * adds at most 768 terms of an fp32 result and 16384 of a bf16 one (which costs
+ * about 7e-7 and, with terms of one sign, 1e-4 of the sum); sums of more terms are
+ * added in fp32 rounded to nearest (to an fp32 output: subnormals may be flushed).
+ * A bf16 result is rounded once. Each call's result is the same bits every time.
+ * offsets[0] may be above 0: rows below it are spare, too. Offsets that do not
+ * ascend within [0, R] set MOE_DEVERR_OFFSETS, and nothing is computed (with
+ * R = 0 nothing runs but wgrad, which clears dW).
+ * A few rows (R <= 128, spread over the experts) take another kernel, with another
+ * order of the sums. R decides that, not the live rows: a step of a few tokens
+ * is fastest with an R close to its rows. */
 MOE_API moe_status moe_grouped_linear(const moe_linear_desc* desc, const void* x,
                                       const int32_t* offsets, const void* W, void* y, void* ws,
                                       size_t ws_bytes, void* stream);

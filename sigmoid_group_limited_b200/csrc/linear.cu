@@ -36,12 +36,17 @@
 // MMAs.
 //
 // The tensor core's fp32 accumulation cuts low bits off at every step, always
-// towards zero: about 1.7e-8 of the sum per 16-deep step, 6e-6 at a depth of
-// 6000. A bf16 result does not see it. An fp32 result is made in passes of at
-// most 768: each pass starts a fresh accumulator and the epilogue adds it to the
-// output in fp32 (rounded to nearest, subnormals flushed), which holds the error at about 8e-7 at
-// any depth. The adds are reductions in L2 (one per element and pass, by the
-// same thread in order, so the result is the same every time).
+// towards zero: per 16-deep step about 1.7e-8 of a sum of terms of both signs,
+// 9e-8 where all have one sign (2.3 % at a depth of 4 M). So a contraction is
+// made in passes, each in a fresh accumulator, added in fp32 (rounded to nearest).
+//   fp32 results: passes of at most 768. The epilogue adds them to the output by
+//   reductions in L2 (subnormals flushed; one per element and pass, by the same
+//   thread in order, so the result is the same every time). A pass costs 6e-7 to
+//   7.5e-7 of the result's norm whatever the depth, and the P adds at most P 2^-24:
+//   7.4e-7 at a depth of 20011, 1.0e-6 at 1 M, 1.5e-6 at 4 M.
+//   bf16 results: passes of at most 16384, about 1e-4 of the sum or 1/40 of the
+//   final rounding; only wgrad is ever deeper. Their sum stays in tensor memory, in the
+//   accumulator that the passes leave free, and is rounded once.
 //
 // What bounds it. Few rows per expert: the weights from HBM (512 experts, 768 x
 // 2560, 32768 rows: 2.23 GB in 346 us, 6.4 TB/s). Hundreds of rows: an M = 256,
@@ -83,7 +88,8 @@ constexpr int kLinEpiWarp0 = 4, kLinEpiWarps = 8;
 constexpr int kLinHalf = 128 * 128;         // one operand's stage: 128 rows of 128 bytes
 constexpr int kLinStage = 2 * kLinHalf;     // A, B
 constexpr int kLinTile = 256;               // features on M, columns on N
-constexpr int kLinChunk = 768;  // most contraction per pass of an fp32 result
+constexpr int kLinChunk = 768;      // most contraction per pass of an fp32 result
+constexpr int kLinChunk16 = 16384;  // and of a bf16 result (wgrad; features end there)
 constexpr int kLinCtrl = 512;
 constexpr int kLinPitch = 80;               // a transposed row: 64 bytes, and 16 against conflicts
 constexpr int kLinStages = 6;
@@ -242,10 +248,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
   };
   // contraction per accumulator: equal shares, in whole 64-deep blocks
   auto chunk_of = [&](int depth) {
-    if (!p.out_f32 || depth <= kLinChunk) return 1 << 30;
-    const int blocks = (depth + 63) / 64, passes = (depth + kLinChunk - 1) / kLinChunk;
+    const int most = p.out_f32 ? kLinChunk : kLinChunk16;
+    if (depth <= most) return 1 << 30;
+    const int blocks = (depth + 63) / 64, passes = (depth + most - 1) / most;
     return (blocks + passes - 1) / passes * 64;
   };
+  // Passes of a bf16 result take one accumulator in turn; the other one holds
+  // their sum, which only the epilogue touches. The next tile takes the first
+  // one, too, so the MMAs are back at the sum's only when the epilogue has left it.
+  auto summed = [&](int depth) { return DIR == kWgrad && !p.out_f32 && depth > kLinChunk16; };
   auto depth_of = [&](const LinTile& t) { return DIR == kWgrad ? t.rows : p.depth; };
 
   if (warp == 0) {
@@ -334,7 +345,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       const uint64_t first_b = DIR == kWgrad ? sdesc_mn128(b0, 8192) : sdesc_k128(b0);
       uint64_t da = first_a, db = first_b;
       int stage = 0;
-      uint32_t phase = 0, used = 0;  // used: accumulators taken so far
+      uint32_t phase = 0;
+      uint32_t buf = 0, uses = 0;  // accumulator; bit b: parity of accumulator b's uses so far
       bool live = true;
       LinTile t;
       if (first < tiles) t = tile_at(first, 0);
@@ -347,14 +359,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         }
         const uint32_t idesc = idesc_bf16(2 * 128, t.n) | major;
         const int chunk = chunk_of(depth);
+        const uint32_t step = summed(depth) ? 0 : 1;  // to the next accumulator
         int left = 0;  // contraction left to this accumulator
         uint32_t d = 0;
         for (int rest = depth; rest > 0; rest -= 64) {
           const bool fresh = left <= 0;
           if (fresh) {  // the next accumulator
-            if (rest < depth) umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
-            const uint32_t buf = used & 1;
-            if (!mbar_wait_cluster(&tempty[buf], ((used >> 1) & 1) ^ 1, abort_flag, p.err,
+            if (rest < depth) umma_commit_pair_mc(&tfull[buf], 0x3), uses ^= 1u << buf, buf ^= step;
+            if (!mbar_wait_cluster(&tempty[buf], ((uses >> buf) & 1) ^ 1, abort_flag, p.err,
                                    MOE_DEVERR_TIMEOUT)) {
               live = false;
               break;
@@ -386,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           if (++stage == kLinStages) stage = 0, phase ^= 1, da = first_a, db = first_b;
         }
         if (!live) break;
-        umma_commit_pair_mc(&tfull[used++ & 1], 0x3);
+        umma_commit_pair_mc(&tfull[buf], 0x3), uses ^= 1u << buf, buf ^= step;
         t = next;
       }
     }
@@ -431,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     const int q = warp & 3, part = (warp - kLinEpiWarp0) / 4;
     uint8_t* tile = epi + (warp - kLinEpiWarp0) * kLinEpi;
     int e = 0;
-    uint32_t used = 0;
+    uint32_t buf = 0, uses = 0;  // as in the MMA issuer
     const int box = kLinBoxRow / (p.out_f32 ? 4 : 2);  // columns of a stored box
     for (int i = first; i < tiles; i += pairs) {
       const LinTile t = tile_at(i, e);
@@ -453,11 +465,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         continue;
       }
       const int chunk = chunk_of(depth);
+      const bool sums = summed(depth);
       bool live = true;
       for (int k0 = 0; k0 == 0 || k0 < depth; k0 += chunk) {
-        const bool add = p.accumulate || k0 > 0;
-        const uint32_t buf = used & 1;
-        if (!mbar_wait(&tfull[buf], (used >> 1) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+        const bool add = p.accumulate || (k0 > 0 && !sums);
+        if (!mbar_wait(&tfull[buf], (uses >> buf) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
           live = false;
           break;
         }
@@ -474,6 +486,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             float v[32];
             tmem_ld16(tq + c0, v);
             if (!p.out_f32) tmem_ld16(tq + c0 + 16, v + 16);
+            if (sums) {  // the sum of the passes, in the other accumulator
+              tmem_ld_wait_for<32>(v);
+              const uint32_t ts = tq + c0 + kLinTile - 2 * buf * kLinTile;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (k0 > 0) {
+                  float w[16];
+                  tmem_ld16(ts + 16 * h, w);
+                  tmem_ld_wait_for<16>(w);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[16 * h + j] += w[j];
+                }
+                if (k0 + chunk < depth) tmem_st16(ts + 16 * h, v + 16 * h);
+              }
+              if (k0 + chunk < depth) continue;
+            }
             if (elect_one()) bulk_wait_read<0>();  // the warp's box is free again
             __syncwarp();
             tmem_ld_wait_for<16>(v);
@@ -558,6 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             }
           }
         }
+        if (sums) tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -566,7 +595,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           if (leader) mbar_arrive(&tempty[buf]);
           else mbar_arrive_cluster_relaxed(at_leader(&tempty[buf]));
         }
-        ++used;
+        uses ^= 1u << buf;
+        if (!sums) buf ^= 1;
       }
       if (!live) break;
     }
