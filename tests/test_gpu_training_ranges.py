@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import sigmoid_group_limited_b200 as sgl
-from tests.test_gpu_training import BF, F32, F64, HYPER, _adam_tensor, _check_adam, _gen, _offsets, _run, _step
+from tests.test_gpu_training import (BF, F32, F64, HYPER, _adam_tensor, _check_adam, _direct, _gen, _offsets,
+                                     _randn, _run, _step)
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,53 @@ def test_wgrad_bf16_of_millions_of_rows():
         want = sum(dy[i:min(i + 2 ** 20, hi)].to(F64).t() @ x[i:min(i + 2 ** 20, hi)].to(F64) for i in range(lo, hi, 2 ** 20))
         err = (dW[e].to(F64) - want) / want
         assert float(err.abs().max()) <= 2.0 ** -8 + 2 ** 14 * 2.0 ** -24 + 257 * 2.0 ** -24
+
+
+def test_wgrad_bf16_of_long_and_short_experts_together():
+    """Experts of one and of several passes, whole and ragged, and none at all,
+    over enough tiles that a pair takes long and short ones in turn; the same
+    bits again. A pass is at most 1024 steps, each off by at most 17 units of
+    2^-23 (16 products and the sum)."""
+    gen = _gen(16)
+    counts, N, K = [16385, 0, 300, 16384, 33333, 7, 49153], 1032, 2568
+    R = sum(counts)
+    dy, x = _randn((R, N), gen), _randn((R, K), gen)
+    off = _offsets(counts)
+    dW = torch.empty(len(counts), N, K, dtype=BF, device="cuda")
+    ws = _run("wgrad", dy, x, off, dW)
+    again = torch.full_like(dW, 7.0)
+    _run("wgrad", dy, x, off, again, ws=ws)
+    assert sgl.moe_linear_read_error(ws) == 0
+    assert torch.equal(dW, again)
+    lo = 0
+    for e, c in enumerate(counts):
+        want = dy[lo:lo + c].to(F64).t() @ x[lo:lo + c].to(F64)
+        err = (dW[e].to(F64) - want).norm(dim=1)
+        assert (err <= (2.0 ** -8 + 1024 * 17 * 2.0 ** -23) * want.norm(dim=1)).all(), e
+        lo += c
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("direction,N,K", [("linear", 72, 16384), ("dgrad", 16384, 72), ("wgrad", 264, 136)])
+def test_fp32_results_do_not_lose_with_depth(direction, N, K, accumulate):
+    """Terms of one sign, a depth of one pass (768) and of many. A sum of passes
+    of one sign is off by no more than its worst pass, relative to itself, and the
+    P adds cost 2^-24 each; twice the first pass's error for the spread
+    between passes. One unbroken sum has an error that grows with the depth: 6e-5
+    at 16384 and 1e-4 at 20011, over twenty times the bound."""
+    gen = _gen(15)
+    depths = (768, 20011) if direction == "wgrad" else (768, 16384)
+    errs = []
+    for depth in depths:
+        counts = [depth, 0, depth] if direction == "wgrad" else [40, 0, 300]
+        n, k = (depth if direction == "dgrad" else N), (depth if direction == "linear" else K)
+        R, E = sum(counts), len(counts)
+        a = _positive((R, k if direction == "linear" else n), gen)
+        b = _positive((R, k) if direction == "wgrad" else (E, n, k), gen)
+        out = torch.zeros({"linear": (R, n), "dgrad": (R, k), "wgrad": (E, n, k)}[direction], device="cuda")
+        ws = _run(direction, a, b, _offsets(counts), out, accumulate)
+        assert sgl.moe_linear_read_error(ws) == 0
+        want, _ = _direct(direction, counts, a, b, torch.zeros_like(out), False)
+        errs.append(float((out.to(F64) - want).norm() / want.norm()))
+    passes = -(-depths[1] // 768)
+    assert errs[1] <= 2 * errs[0] + passes * 2.0 ** -24, errs
