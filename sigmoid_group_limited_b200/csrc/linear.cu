@@ -69,11 +69,13 @@
 //   2      wgrad: zeroes the rows behind an expert's last
 //   3      idle
 //   4..11  epilogue, two warps per TMEM lane quarter, alternate column chunks
-// Every wait is bounded and raises the error word.
+// Every wait is bounded and raises the error word; the warps that wait together
+// (2, 4..11) give up together.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "ffn_common.cuh"
@@ -111,6 +113,10 @@ struct LinParams {
   const int32_t* offsets;
   void* out;
   int32_t* err;
+  // test hooks of the waits: their limit in cycles, and arrivals added to those
+  // that free an accumulator (some that never come make the waits run out)
+  long long wait_limit;
+  int ready_extra;
 };
 
 struct LinMaps {
@@ -171,8 +177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       mbar_init(&tail[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);                  // multicast commit
-      mbar_init(&tempty[a], 2 * kLinEpiWarps);  // the epilogue warps of both CTAs
+      mbar_init(&tfull[a], 1);  // multicast commit
+      mbar_init(&tempty[a], 2 * kLinEpiWarps + p.ready_extra);  // the epilogue warps of both CTAs
     }
     *abort_flag = 0;
     *bad = count[0] = count[1] = 0;
@@ -281,7 +287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const uint64_t pa = DIR != kWgrad && s_off[t.e + 1] - s_off[t.e] <= wide ? pol_w : pol;
         const int row0 = s_off[t.e];
         for (int k0 = 0; k0 < depth; k0 += 64) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit)) {
             live = false;
             break;
           }
@@ -323,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       }
       // every stage must be released by the MMA before teardown
       for (int i = 0; i < kLinStages && live; ++i) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
+        if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit)) break;
         if (++stage == kLinStages) stage = 0, phase ^= 1;
       }
       // after a timeout: time for the copies and MMAs in flight to end (they take microseconds)
@@ -367,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           if (fresh) {  // the next accumulator
             if (rest < depth) umma_commit_pair_mc(&tfull[buf], 0x3), uses ^= 1u << buf, buf ^= step;
             if (!mbar_wait_cluster(&tempty[buf], ((uses >> buf) & 1) ^ 1, abort_flag, p.err,
-                                   MOE_DEVERR_TIMEOUT)) {
+                                   MOE_DEVERR_TIMEOUT, p.wait_limit)) {
               live = false;
               break;
             }
@@ -376,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
           }
           left -= 64;
           if (!(DIR == kWgrad  // only there does the other CTA write what this one then reads
-                    ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT)
-                    : mbar_wait(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT))) {
+                    ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit)
+                    : mbar_wait(&full[stage], phase, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit))) {
             live = false;
             break;
           }
@@ -415,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         const int blocks = (t.rows + 63) / 64, rest = t.rows % 64;
         if (rest % 16 != 0) {
           const int s = (stage + blocks - 1) % kLinStages;
-          if (!mbar_wait(&tail[s], (seen >> s) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) break;
+          if (!mbar_wait_warp(&tail[s], (seen >> s) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit)) break;
           seen ^= 1u << s;
           // whole 128-byte rows: the swizzle moves pieces inside a row only
           uint8_t* base = smem + s * kLinStage;
@@ -469,11 +475,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
       bool live = true;
       for (int k0 = 0; k0 == 0 || k0 < depth; k0 += chunk) {
         const bool add = p.accumulate || (k0 > 0 && !sums);
-        if (!mbar_wait(&tfull[buf], (uses >> buf) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT)) {
+        if (!mbar_wait_warp(&tfull[buf], (uses >> buf) & 1, abort_flag, p.err, MOE_DEVERR_TIMEOUT, p.wait_limit)) {
           live = false;
           break;
         }
-        __syncwarp();  // tensor-memory reads are warp-wide
         tc_fence_after();
         // the pass before has reached the output (bulk stores keep no order)
         if (DIR == kWgrad && k0 > 0 && elect_one()) bulk_wait<0>();
@@ -678,6 +683,10 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
   p.offsets = offsets;
   p.out = out;
   p.err = err;
+  p.wait_limit = kWaitLimitCycles;
+  if (const char* v = getenv("SGL_MOE_TEST_WAIT_CYCLES")) p.wait_limit = strtoll(v, nullptr, 10);
+  if (const char* v = getenv("SGL_MOE_TEST_READY_EXTRA"))
+    p.ready_extra = static_cast<int>(max(0L, min(1000L, strtol(v, nullptr, 10))));
   LinMaps m;
   memset(&m, 0, sizeof(m));
   bool ok = true;

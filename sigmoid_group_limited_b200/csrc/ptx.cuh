@@ -74,20 +74,30 @@ constexpr long long kWaitLimitCycles = 4000000000LL;
 
 // Bounded wait on the phase with the given parity. On timeout, raises the
 // CTA-wide abort flag and the global error word; once the abort flag is up,
-// every other wait in the CTA returns false at once.
+// every other wait in the CTA returns false at once. The verdict is each lane's
+// own: a warp that goes on together asks all its lanes (mbar_wait_warp).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
-                                          volatile int* abort_flag, int* err, int code) {
+                                          volatile int* abort_flag, int* err, int code,
+                                          long long limit = kWaitLimitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       *abort_flag = 1;
       if (err) atomicExch(err, code);
       return false;
     }
   }
+}
+
+// The same for a converged warp: true in every lane or in none (while the wait
+// gives up, one lane may still see the phase complete and another the abort flag).
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               volatile int* abort_flag, int* err, int code,
+                                               long long limit = kWaitLimitCycles) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code, limit));
 }
 
 // ------------------------------------------------------------------ TMA
@@ -257,13 +267,14 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 // Bounded wait with the same abort protocol as mbar_wait, cluster-scope acquire.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort_flag, int* err, int code) {
+                                                  volatile int* abort_flag, int* err, int code,
+                                                  long long limit = kWaitLimitCycles) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitLimitCycles) {
+    if (clock64() - t0 > limit) {
       *abort_flag = 1;
       if (err) atomicExch(err, code);
       return false;

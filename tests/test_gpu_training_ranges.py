@@ -1,11 +1,13 @@
 """The training operators at the ends of their ranges: gradient scales far
-from one, long contractions."""
+from one, long contractions, waits that give up."""
+import time
+
 import pytest
 import torch
 
 import sigmoid_group_limited_b200 as sgl
-from tests.test_gpu_training import (BF, F32, F64, HYPER, _adam_tensor, _check_adam, _direct, _gen, _offsets,
-                                     _randn, _run, _step)
+from tests.test_gpu_training import (BF, F32, F64, HYPER, _adam_tensor, _check, _check_adam, _direct, _gen, _offsets,
+                                     _product, _randn, _run, _step)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +105,29 @@ def test_fp32_results_do_not_lose_with_depth(direction, N, K, accumulate):
         errs.append(float((out.to(F64) - want).norm() / want.norm()))
     passes = -(-depths[1] // 768)
     assert errs[1] <= 2 * errs[0] + passes * 2.0 ** -24, errs
+
+
+# ------------------------------------------------------------------ waits that give up
+@pytest.mark.parametrize("direction,counts,N,K,out", [
+    ("linear", [40, 0, 300], 264, 2560, F32), ("dgrad", [40, 0, 300], 2560, 264, F32),
+    ("wgrad", [2500, 37, 0, 900], 264, 136, F32), ("wgrad", [40007, 37], 264, 136, BF)])
+def test_waits_run_out_and_report(direction, counts, N, K, out, monkeypatch):
+    """The accumulators are never free again (their barriers wait for an arrival
+    that does not come) and the waits' limit is about 1 ms: every role gives up,
+    the call returns with the error word set, and the next one is right."""
+    _check(direction, counts, N, K, out=out, seed=17)
+    a, b, o = _product(direction, counts, N, K, out=out, seed=17)
+    off = _offsets(counts)
+    ws = sgl.alloc_linear_workspace(len(counts), a.shape[0], 8, 8)
+    torch.cuda.synchronize()
+    monkeypatch.setenv("SGL_MOE_TEST_WAIT_CYCLES", "2000000")
+    monkeypatch.setenv("SGL_MOE_TEST_READY_EXTRA", "1")
+    t0 = time.perf_counter()
+    _run(direction, a, b, off, o, ws=ws)
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 5.0
+    monkeypatch.delenv("SGL_MOE_TEST_WAIT_CYCLES")
+    monkeypatch.delenv("SGL_MOE_TEST_READY_EXTRA")
+    assert sgl.moe_linear_read_error(ws) == 2            # MOE_DEVERR_TIMEOUT
+    assert sgl.moe_linear_read_error(ws) == 0
+    _check(direction, counts, N, K, out=out, seed=17)
