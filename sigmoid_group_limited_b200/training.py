@@ -73,6 +73,8 @@ def _rows(t: torch.Tensor, name: str, dtype=torch.bfloat16):
         ld = w  # the stride of a single row says nothing
     if one != 1 and w > 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
+    if (n | w | ld) >> 31:  # ctypes would cut them to 32 bits without a word
+        raise ValueError(f"{name}: rows, width and row stride must fit in 31 bits")
     return n, w, ld
 
 
@@ -121,6 +123,8 @@ def _call(fn, where: str, tensors, stream, *args) -> None:
 
 # ------------------------------------------------------------------ grouped products
 def linear_workspace_size(E: int, R: int, N: int, K: int) -> int:
+    if (E | R | N | K) >> 31:  # negative ones, too
+        raise MoEError(-1, "moe_linear_workspace_size")
     d = moe_linear_desc(E, R, N, K, K, N, MOE_T_BF16, 0)
     n = lib().moe_linear_workspace_size(ctypes.byref(d))
     if n == 0:
@@ -136,10 +140,11 @@ def alloc_linear_workspace(E: int, R: int, N: int, K: int, device=None) -> torch
 
 
 def _offsets(offsets: torch.Tensor) -> int:
-    if offsets.dim() != 1 or offsets.numel() < 2:
+    E = offsets.numel() - 1
+    if offsets.dim() != 1 or E < 1 or E >> 31:
         raise ValueError("offsets: expected E + 1 entries")
     _flat(offsets, "offsets", torch.int32)
-    return offsets.numel() - 1
+    return E
 
 
 def _weights(W: torch.Tensor, name: str, E: int, types):
@@ -244,6 +249,8 @@ def _weight_args(d, w, perm, rows):
         return None, None, 0, rp
     if perm is None:
         return _flat(w, "w", torch.float32, d.R, True), None, 0, rp
+    if w.numel() >> 31:
+        raise ValueError("w: its size must fit in 31 bits")
     return _flat(w, "w", torch.float32), _flat(perm, "perm", torch.int32, d.R, True), w.numel(), rp
 
 
