@@ -13,11 +13,14 @@
 // and the next row's weight loaded ahead change that by less than 5 %. A group of G lanes owns a row (so dw is one shuffle reduction,
 // in a fixed order) and moves 8 features (16 bytes) per lane and tensor.
 // Everything between the loads and the one rounding of each output is fp32;
-// the exponential is the hardware one (a few ulp, far below bf16's half ulp).
+// the exponential is the hardware one (see sigmoid_fast for its error, which is
+// largest, 5e-6, where it counts least; bf16's half step is 2^-8).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -70,10 +73,29 @@ __device__ __forceinline__ float clamp_nan(float v, float L) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-L));
   return r;
 }
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// s = 1 / (1 + e^-a). The exponential's relative error is about (|a| + 2) 2^-24,
+// from the rounding of its argument, and counts by 1 - s. Below kFarGate (DEEP)
+// s is at the end of fp32's normal numbers or below, where 1 + e^-a overflows
+// and the reciprocal is cut to zero, but s a is still a number that bf16 holds:
+// there s = e^a, formed 2^24 times too large (spacing 2^-149, zero from -104 on).
+constexpr float kFarGate = -87.f, kLog2e = 1.44269504f;
+template <bool DEEP>
 __device__ __forceinline__ float sigmoid_fast(float a) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-a)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(-kLog2e * a)));
+  if (DEEP && a < kFarGate) r = exp2_fast(fmaf(kLog2e, a, 24.f)) * 5.9604644775390625e-8f;
   return r;
+}
+// The least of 8 bf16 values (of those that are not NaN).
+__device__ __forceinline__ float least8(const uint4& v) {
+  const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&v);
+  const float2 m = __bfloat1622float2(__hmin2(__hmin2(b[0], b[1]), __hmin2(b[2], b[3])));
+  return fminf(m.x, m.y);
 }
 
 // Routing weight of row r and where its gradient goes (-1: nowhere).
@@ -121,20 +143,24 @@ __global__ void __launch_bounds__(kActThreads, 4) act_kernel(const ActParams p) 
         unpack8(qg[k], g);
         unpack8(qu[k], u);
         if (BWD) unpack8(qd[k], dh);
+        auto compute = [&](auto deep) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = clamp_nan(g[i], p.limit), b = clamp_nan(u[i], p.limit);
-          const float s = sigmoid_fast(a);
-          const float silu = a * s;
-          if (!BWD) {
-            o[i] = w * silu * b;
-          } else {
-            sum += dh[i] * (silu * b);
-            const float wd = w * dh[i];
-            o[i] = fabsf(g[i]) > p.limit ? 0.f : wd * b * (s + silu * (1.f - s));
-            o2[i] = fabsf(u[i]) > p.limit ? 0.f : wd * silu;
+          for (int i = 0; i < 8; ++i) {
+            const float a = clamp_nan(g[i], p.limit), b = clamp_nan(u[i], p.limit);
+            const float s = sigmoid_fast<decltype(deep)::value>(a);
+            const float silu = a * s;
+            if (!BWD) {
+              o[i] = w * silu * b;
+            } else {
+              sum += dh[i] * (silu * b);
+              const float wd = w * dh[i];
+              o[i] = fabsf(g[i]) > p.limit ? 0.f : wd * b * (s + silu * (1.f - s));
+              o2[i] = fabsf(u[i]) > p.limit ? 0.f : wd * silu;
+            }
           }
-        }
+        };
+        if (least8(qg[k]) < kFarGate && p.limit > -kFarGate) compute(std::true_type());  // rare
+        else compute(std::false_type());
         if (!BWD) {
           store8(p.h, r * p.ld_h + 8 * c, pack8(o));
         } else {

@@ -1,5 +1,5 @@
 """The training operators at the ends of their ranges: gradient scales far
-from one, long contractions, waits that give up."""
+from one, gates far below zero, long contractions, waits that give up."""
 import time
 
 import pytest
@@ -31,6 +31,50 @@ def test_adamw_scales_the_gradient_before_it_squares_it(q8, g, power, dyn):
     before = _step([t], **kw)[0]
     assert torch.isfinite(t["v"].float()).all() and torch.isfinite(t["p"].float()).all()
     _check_adam(before, t, HYPER, gs)
+
+
+# ------------------------------------------------------------------ SwiGLU
+def test_swiglu_gates_far_below_zero():
+    """No limit and gates down to -100: the sigmoid is below the normal
+    numbers of fp32, its product with a large up value is not. e^a costs |a|
+    2^-24 for its argument and a few 2^-23, and below 2^-126 a spacing of 2^-149;
+    below -103.3 the sigmoid is zero."""
+    gen = _gen(13)
+    R, I = 64, 264
+    g = -(torch.rand(R, I, generator=gen, device="cuda") * 22 + 80).to(BF)
+    g[:, :8] = torch.tensor([-200.0, -3e38, 80.0, 100.0, 3e38, 0.0, -0.0, -1e-30], device="cuda").to(BF)
+    u = (_randn((R, I), gen, F32) * 2.0 ** 20).to(BF)
+    dh = _randn((R, I), gen)
+    w = torch.rand(R, generator=gen, device="cuda") + 0.5
+    h, dg, du, dw = torch.empty_like(g), torch.empty_like(g), torch.empty_like(g), torch.empty_like(w)
+    u[:, 4] = 1.0                                        # 3e38 w: stays finite
+    w[:] = w.clamp(max=1.0)
+    sgl.moe_swiglu(g, u, h, w=w)
+    sgl.moe_swiglu_backward(dh, g, u, dg, du, w=w, dw=dw)
+    a, b, d, ww = g.to(F64), u.to(F64), dh.to(F64), w.to(F64)[:, None]
+    s = torch.sigmoid(a)
+    rel, low = 128 * 2.0 ** -24 + 8 * 2.0 ** -23, 2.0 ** -149
+    bf = 2.0 ** -134                                     # half the spacing of bf16 below its normal numbers
+
+    def near(got, want, terms, floor):
+        tol = 2.0 ** -8 * want.abs() + rel * terms + floor + bf
+        past = want.abs() > torch.finfo(BF).max * (1 + 2.0 ** -8)        # no bf16 value: infinite
+        assert torch.equal(got[past].to(F64), want[past].sign() * float("inf"))
+        bad = ((got.to(F64) - want).abs() > tol) & ~past
+        assert not bad.any(), (a[bad][:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())
+
+    near(h, ww * a * s * b, (ww * a * s * b).abs(), (ww * a * b).abs() * low)
+    near(du, ww * d * a * s, (ww * d * a * s).abs(), (ww * d * a).abs() * low)
+    t = (ww * d * b).abs()
+    near(dg, ww * d * b * s * (1 + a * (1 - s)), t * s * (1 + a.abs() * (1 - s)), t * (1 + a.abs()) * low)
+    # the far gates alone
+    far = torch.zeros_like(g)
+    far[:] = -88.0
+    sgl.moe_swiglu_backward(dh, far, u, dg, du, w=w, dw=dw)
+    a = far.to(F64)
+    terms = d * a * torch.sigmoid(a) * b
+    err = (dw.to(F64) - terms.sum(1)).abs()
+    assert (err <= (rel + I * 2.0 ** -24) * terms.abs().sum(1) + (d * a * b).abs().sum(1) * low).all()
 
 
 # ------------------------------------------------------------------ long contractions
