@@ -156,10 +156,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Square root and reciprocal within about 1 ulp, subnormals taken as zero.
+// Square root and reciprocal within about 1 ulp; of a subnormal v the root is
+// zero unless LOW (its root is a normal number), the reciprocal infinite.
+template <bool LOW>
 __device__ __forceinline__ float sqrt_fast(float v) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  if (LOW) asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 __device__ __forceinline__ float rcp_fast(float v) {
@@ -232,9 +235,10 @@ struct AdamStep {
 };
 
 // `count` blocks of one tensor from blk on, all of them whole (FULL) or the one
-// short block at its end; PF32, MASTER, GF32, Q8: its types. With 8-bit states
+// short block at its end; PF32, MASTER, GF32, Q8: its types; LOW: subnormal second
+// moments count (see launch_list). With 8-bit states
 // the next block's loads are under way while a block is computed.
-template <bool PF32, bool MASTER, bool GF32, bool Q8, bool FULL>
+template <bool PF32, bool MASTER, bool GF32, bool Q8, bool LOW, bool FULL>
 __device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamStep& h, long long blk, int count,
                                          int lane) {
   constexpr int BP = PF32 ? 4 : 2, BG = GF32 ? 4 : 2, BS = Q8 ? 1 : 4;
@@ -290,7 +294,7 @@ __device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamStep& h,
         m[i] = h.b1 * m[i] + h.b1c * g[i];
         v[i] = h.b2 * v[i] + h.b2c * (g[i] * g[i]);
       }
-      root[i] = sqrt_fast(v[i]);
+      root[i] = sqrt_fast<LOW>(v[i]);
       p[i] = p[i] * keep - h.step * (m[i] * rcp_fast(root[i] * h.inv2 + h.eps));
     }
     if (MASTER) {
@@ -326,15 +330,15 @@ __device__ __forceinline__ void adam_run(const AdamTensor& t, const AdamStep& h,
 }
 
 // Blocks [blk, end) of one tensor.
-template <bool PF32, bool MASTER, bool GF32, bool Q8>
+template <bool PF32, bool MASTER, bool GF32, bool Q8, bool LOW>
 __device__ __forceinline__ void adam_blocks(const AdamTensor& t, const AdamStep& h, long long blk,
                                             long long end, int lane) {
   const long long whole = min(end, t.n / kBlock);
-  if (blk < whole) adam_run<PF32, MASTER, GF32, Q8, true>(t, h, blk, static_cast<int>(whole - blk), lane);
-  if (whole < end) adam_run<PF32, MASTER, GF32, Q8, false>(t, h, whole, 1, lane);
+  if (blk < whole) adam_run<PF32, MASTER, GF32, Q8, LOW, true>(t, h, blk, static_cast<int>(whole - blk), lane);
+  if (whole < end) adam_run<PF32, MASTER, GF32, Q8, LOW, false>(t, h, whole, 1, lane);
 }
 
-template <bool Q8, int CAP>
+template <bool Q8, bool LOW, int CAP>
 __global__ void __launch_bounds__(kAdamThreads, kAdamCtas)
     adamw_kernel(const __grid_constant__ AdamParams<CAP> P) {
   pdl_wait();
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas)
     const long long end = min(blk + P.span, (t.n + kBlock - 1) / kBlock);
     switch (t.types) {
 #define ADAM_CASE(p, m, g) \
-  case (p) | (m) << 1 | (g) << 2: adam_blocks<p, m, g, Q8>(t, h, blk, end, lane); break
+  case (p) | (m) << 1 | (g) << 2: adam_blocks<p, m, g, Q8, LOW>(t, h, blk, end, lane); break
       ADAM_CASE(0, 0, 0);
       ADAM_CASE(0, 0, 1);
       ADAM_CASE(0, 1, 0);
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamCtas)
 }
 
 // The tensors with (Q8) or without 8-bit states, as many per launch as fit.
-template <bool Q8, int CAP>
+template <bool Q8, bool LOW, int CAP>
 cudaError_t launch_states(AdamParams<CAP>& P, const moe_adamw_cfg& c, const moe_adamw_tensor* t, int n,
                           cudaStream_t s) {
   constexpr int warps = kAdamThreads / 32;
@@ -397,7 +401,7 @@ cudaError_t launch_states(AdamParams<CAP>& P, const moe_adamw_cfg& c, const moe_
       P.first[k + 1] = P.first[k] + (P.t[k].n + kBlock * P.span - 1) / (kBlock * P.span);
     // more CTAs than run at once: the late ones even out the early ones' ends
     const long long need = (P.first[P.count] + warps - 1) / warps, most = num_sms() * 8LL;
-    const cudaError_t e = launch_pdl(adamw_kernel<Q8, CAP>, dim3(static_cast<unsigned>(need < most ? need : most)),
+    const cudaError_t e = launch_pdl(adamw_kernel<Q8, LOW, CAP>, dim3(static_cast<unsigned>(need < most ? need : most)),
                                      dim3(kAdamThreads), 0, s, P);
     if (e != cudaSuccess) return e;
   }
@@ -417,8 +421,14 @@ cudaError_t launch_list(const moe_adamw_cfg& c, const moe_adamw_tensor* t, int n
   P.b2 = static_cast<float>(c.beta2);
   P.b2c = static_cast<float>(1.0 - c.beta2);
   P.eps = static_cast<float>(c.eps);
-  const cudaError_t e = launch_states<false>(P, c, t, n, s);
-  return e != cudaSuccess ? e : launch_states<true>(P, c, t, n, s);
+  // The root of a subnormal v, at most 2^-63, counts beside an eps below 2^24
+  // times that (times the smallest sqrt(1 - beta2^step)). fp32 states, bound by memory, take
+  // subnormals in their stride; 8-bit states, bound by issue, pay for them (377 M
+  // elements 783 us for 751), so only a step with such an eps does.
+  const bool low = c.eps * sqrt(1.0 - c.beta2) < 0x1p-39;
+  const cudaError_t e = launch_states<false, true>(P, c, t, n, s);
+  if (e != cudaSuccess) return e;
+  return low ? launch_states<true, true>(P, c, t, n, s) : launch_states<true, false>(P, c, t, n, s);
 }
 
 }  // namespace

@@ -1,12 +1,12 @@
 """The training operators at the ends of their ranges: gradient scales far
-from one, gates far below zero, long contractions, waits that give up."""
+from one, second moments below the normal numbers, gates far below zero, long contractions, waits that give up."""
 import time
 
 import pytest
 import torch
 
 import sigmoid_group_limited_b200 as sgl
-from tests.test_gpu_training import (BF, F32, F64, HYPER, _adam_tensor, _check, _check_adam, _direct, _gen, _offsets,
+from tests.test_gpu_training import (BF, F8, F32, F64, HYPER, _adam_tensor, _check, _check_adam, _direct, _gen, _offsets,
                                      _product, _randn, _run, _step)
 
 pytestmark = pytest.mark.gpu
@@ -31,6 +31,34 @@ def test_adamw_scales_the_gradient_before_it_squares_it(q8, g, power, dyn):
     before = _step([t], **kw)[0]
     assert torch.isfinite(t["v"].float()).all() and torch.isfinite(t["p"].float()).all()
     _check_adam(before, t, HYPER, gs)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_adamw_second_moments_below_the_normal_numbers(q8):
+    """v' between 2^-130 and 2^-126 and no eps: the update is m over its root,
+    not over zero. There v holds 19 bits or more, so its two or three
+    roundings are 2^-19 of it at most, the root's 2^-20 each."""
+    gen = _gen(12)
+    n, beta1, beta2, lr, step = 2048, 0.9, 0.95, 1e-3, 5
+    root = torch.exp2(torch.rand(n, generator=gen, device="cuda", dtype=F64) * 2 - 65)   # 2^-65 .. 2^-63
+    t = dict(p=_randn(n, gen, F32), g=torch.zeros(n, device="cuda"))
+    if q8:
+        top = 2.0 ** -63 / 448
+        t["v"] = (root / 2.0 ** -63 * 448).to(F8)
+        t["m"] = (torch.rand(n, generator=gen, device="cuda") * 300 + 100).to(F8)
+        t["v_scale"] = torch.full((n // 256,), top, device="cuda", dtype=F64).float()
+        t["m_scale"] = torch.full((n // 256,), 2.0 ** -73, device="cuda")
+        m = t["m"].to(F64) * 2.0 ** -73
+        v = (t["v"].to(F64) * t["v_scale"].to(F64).repeat_interleave(256)) ** 2
+    else:
+        t["m"] = (torch.rand(n, generator=gen, device="cuda") + 0.5) * 2.0 ** -64
+        t["v"] = (root * root).float()
+        m, v = t["m"].to(F64), t["v"].to(F64)
+    p0 = t["p"].to(F64)
+    sgl.moe_adamw_step(sgl.make_adamw_tensors([t]), lr=lr, beta1=beta1, beta2=beta2, eps=0.0, step=step)
+    up = lr / (1 - beta1 ** step) * beta1 * m / (beta2 * v / (1 - beta2 ** step)).sqrt()
+    assert float(up.abs().min()) > 1e-4                  # far above the rounding of p
+    assert ((t["p"].to(F64) - (p0 - up)).abs() <= 2 * 2.0 ** -24 * p0.abs() + 6 * 2.0 ** -20 * up.abs()).all()
 
 
 # ------------------------------------------------------------------ SwiGLU
