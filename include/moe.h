@@ -396,8 +396,11 @@ typedef struct moe_adamw_cfg {
 /* One AdamW step over n_tensors tensors (host array, read during the call):
  *   g' = grad_scale g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   p = p (1 - lr wd) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
- * in fp32 (a v below 2^-126 counts as zero there), p taken from master where there is one. The update uses m and v
- * before they are rounded to 8 bits. A non-finite gradient makes its element
+ * in fp32, p taken from master where there is one; g' is rounded to fp32 before
+ * it is squared. eps is 0 or at least 2^-126 (what fp32 holds as a normal
+ * number); with 0 an element whose v is zero becomes non-finite, as in the
+ * formula. The update uses m and v before they are rounded to 8 bits. A
+ * non-finite gradient makes its element
  * non-finite, with 8-bit states its block. Tensors must not overlap. */
 MOE_API moe_status moe_adamw_step(const moe_adamw_cfg* cfg, const moe_adamw_tensor* tensors,
                                   int32_t n_tensors, void* stream);

@@ -136,6 +136,7 @@ moe_status moe_adamw_step(const moe_adamw_cfg* cfg, const moe_adamw_tensor* tens
   if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0))
     return MOE_ERR_CFG;
   if (!(cfg->eps >= 0.0) || !isfinite(cfg->eps) || !isfinite(cfg->weight_decay)) return MOE_ERR_CFG;
+  if (cfg->eps > 0.0 && cfg->eps < 0x1p-126) return MOE_ERR_CFG;  // its fp32 reciprocal may be infinite
   if (cfg->dyn == nullptr &&
       (cfg->step < 1 || !isfinite(cfg->lr) || !isfinite(cfg->grad_scale)))
     return MOE_ERR_CFG;

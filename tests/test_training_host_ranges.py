@@ -1,4 +1,6 @@
 """The training operators' binding at the ends of its ranges, without a GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -40,3 +42,13 @@ def test_sizes_past_31_bits_are_refused():
     for sizes in ((1, R, 8, 8), (2 ** 32 + 1, 8, 8, 8), (1, 8, 2 ** 32 + 8, 8), (1, 8, 8, 2 ** 32 + 8), (1, -2 ** 33 + 5, 8, 8)):
         with pytest.raises(sgl.MoEError):
             sgl.linear_workspace_size(*sizes)
+
+
+@pytest.mark.parametrize("eps,status", [(1e-39, -1), (1e-50, -1), (5e-324, -1), (-0.0, -2), (0.0, -2), (2.0 ** -126, -2)])
+def test_adamw_eps_is_zero_or_a_normal_number_of_fp32(eps, status):
+    """A smaller eps would be divided by as an infinity's reciprocal, and an
+    element that never had a gradient would become NaN. -2: what comes after the
+    check, a tensor without addresses."""
+    cfg = sgl.moe_adamw_cfg(1e-3, 0.9, 0.99, eps, 0.1, 1.0, 1, None)
+    none = (sgl.moe_adamw_tensor * 1)(sgl.moe_adamw_tensor(None, None, None, None, None, None, None, 10, 0, 0, 0, 1.0))
+    assert sgl.lib().moe_adamw_step(ctypes.byref(cfg), none, 1, None) == status
