@@ -61,6 +61,48 @@ def test_adamw_second_moments_below_the_normal_numbers(q8):
     assert ((t["p"].to(F64) - (p0 - up)).abs() <= 2 * 2.0 ** -24 * p0.abs() + 6 * 2.0 ** -20 * up.abs()).all()
 
 
+def test_adamw_codes_with_zeros_and_a_gradient_scale():
+    """8-bit states where much is zero (experts without rows, the first step):
+    whole blocks, single elements, zero gradients on states that are not. Codes
+    and scales equal those of the formula with every fp32 operation rounded by
+    itself, under a gradient scale, too."""
+    gen = _gen(18)
+    n = 300 * 256 + 100
+    blocks = -(-n // 256)
+    t = _adam_tensor(n, gen, BF, F32, True)
+    for k in ("m", "v"):
+        t[k].view(torch.uint8)[:100 * 256] = 0               # idle from the start
+        t[k].view(torch.uint8)[torch.rand(n, generator=gen, device="cuda") < 0.5] = 0
+    h = sgl.make_adamw_tensors([t])
+
+    def rows(x):
+        full = torch.zeros(blocks * 256, device="cuda")
+        full[:n] = x.to(F32)
+        return full.view(-1, 256)
+
+    gs = torch.tensor(0.37, device="cuda")
+    for step in (1, 2, 3):
+        t["g"].copy_(_randn(n, gen, F32, 1e-3))
+        t["g"][:50 * 256] = 0
+        t["g"][torch.rand(n, generator=gen, device="cuda") < 0.5] = 0
+        g = rows(t["g"]) * gs
+        m, v = rows(t["m"]) * t["m_scale"][:, None], rows(t["v"]) * t["v_scale"][:, None]
+        m = 0.9 * m + (1 - 0.9) * g
+        v = 0.95 * (v * v) + (1 - 0.95) * (g * g)
+        sgl.moe_adamw_step(h, lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=step, grad_scale=float(gs))
+        assert torch.isfinite(t["p"].float()).all()
+        for key, x in (("m", m), ("v", v.sqrt())):
+            top = x.abs().amax(1, keepdim=True)
+            code = (x * torch.where(top > 0, top.reciprocal() * 448, 0.0)).to(F8)
+            if key == "v":
+                code = torch.where((x > 0) & (code.to(F32) == 0), 2.0 ** -9, code.to(F32)).to(F8)
+            # a product of zero and a negative number is -0, with or without the sum's sign
+            same = t[key].view(torch.uint8) == code.view(-1)[:n].view(torch.uint8)
+            zero = (t[key].to(F32) == 0) & (code.view(-1)[:n].to(F32) == 0)
+            assert (same | zero).all(), (key, step)
+            assert torch.equal(t[key + "_scale"], (top * torch.tensor(1.0 / 448, device="cuda")).view(-1)), (key, step)
+
+
 # ------------------------------------------------------------------ SwiGLU
 def test_swiglu_gates_far_below_zero():
     """No limit and gates down to -100: the sigmoid is below the normal
