@@ -8,10 +8,12 @@
 //   dw = sum_i dh a s b
 //
 // Both are bound by memory: 6 bytes per element forward (g, u in, h out), 10
-// backward; 32768 x 768 take 28.5 us (5.3 TB/s) and 48 us (5.1 TB/s), launch
+// backward; 32768 x 768 take 28.5 us (5.3 TB/s) and 48.3 us (5.2 TB/s), launch
 // included. Fewer or more pieces under way per lane, two to six blocks an SM
-// and the next row's weight loaded ahead change that by less than 5 %. A group of G lanes owns a row (so dw is one shuffle reduction,
-// in a fixed order) and moves 8 features (16 bytes) per lane and tensor.
+// and the next row's weight loaded ahead change that by less than 5 %. A group of G
+// lanes owns a row (so dw is one shuffle reduction, in a fixed order) and moves 8
+// features (16 bytes) per lane and tensor; rows wider than 2048 take a block each
+// (8192 x 4096, in a graph: 34.7 us forward, 60.1 backward, 5.8 and 5.6 TB/s).
 // Everything between the loads and the one rounding of each output is fp32;
 // the exponential is the hardware one (see sigmoid_fast for its error, which is
 // largest, 5e-6, where it counts least; bf16's half step is 2^-8).

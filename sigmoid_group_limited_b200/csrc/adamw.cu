@@ -10,8 +10,9 @@
 // by one lane. The arithmetic of 8-bit states fills most of the issue slots, so
 // it is kept short: roots and reciprocals are the hardware's wherever they do
 // not decide a code. 144 M elements with fp32 states: 668 us, 6.0 TB/s; 377 M
-// with 8-bit states: 766 us sustained, 690 us in short runs, 5.0 to 5.5 TB/s at
-// 57 instructions an element and 0.84 of the issue slots.
+// with 8-bit states: 766 us sustained, 702 us in short runs, 5.0 to 5.4 TB/s at
+// 58 instructions an element and 0.83 of the issue slots; with second moments that
+// are all zero 938 us (see root_codes).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -203,8 +204,9 @@ __device__ __forceinline__ Piece<1> to_codes(const float* y) {
 // Codes of the square roots of 8 second moments. root: within an ulp or two,
 // enough for a code unless the value lies at a border between two codes;
 // there (low 19 mantissa bits near zero, 1 of 30000 values) the exact root
-// decides, so that the codes are those of the definition. What is not zero
-// gets at least the smallest code.
+// decides, so that the codes are those of the definition. A zero counts as such a
+// border, too, and costs its lane the exact roots. What is not zero gets at least
+// the smallest code.
 __device__ __forceinline__ Piece<1> root_codes(const float* v, const float* root, float inv) {
   float y[8];
   uint32_t near = 0x7ffffu;

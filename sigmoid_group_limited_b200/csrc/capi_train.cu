@@ -1,5 +1,6 @@
 // capi_train.cu - C-ABI of the training operators (include/moe.h): argument
-// validation, then the launch. Nothing here throws, allocates or keeps state.
+// validation, then the launch. No device memory is allocated, and only constants of
+// a device (its kernels' attributes) are kept.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

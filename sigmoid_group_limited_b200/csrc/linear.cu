@@ -663,10 +663,14 @@ cudaError_t launch_grouped_linear(const moe_linear_desc& d, LinearDir dir, const
                                   const void* b, const int32_t* offsets, void* out, int32_t* err,
                                   cudaStream_t s) {
   // A few rows, spread over the experts: bound by the weights of rows that share
-  // none, see linear_few.cu. Measured with 768 x 2560 weights: 8 rows of 512
-  // experts 14 us there and 34 here, 64 rows 43 and 64, 128 rows 75 and 91
-  // (2560 x 768: 83 and 84); 8 rows of a single expert 13 and 18, 32 rows 18
-  // and 18, 64 rows 28 and 19.
+  // none, see linear_few.cu. Calls back to back in a graph, weights not in L2, there
+  // and here, us:
+  //   rows                          8           16           32           64           128
+  //   768 x 2560, an expert each  9.5, 28.6  14.7, 29.9  25.0, 51.2  44.2, 65.2  82.6, 101.5
+  //   2560 x 768, an expert each  9.0, 37.6  14.0, 42.8  24.2, 50.3  42.4, 63.3  80.4,  91.2
+  //   768 x 2560, one expert      6.7, 13.4  11.2, 13.4    - , 13.5    - , 13.7    - ,  14.6
+  //   2560 x 768, one expert      6.7,  8.2  10.6,  8.2    - ,  8.3    - ,  8.5    - ,   9.1
+  // R is the rows' capacity: the live rows are known on the device only.
   if (dir == kFwd && d.R <= kFewMaxRows && (d.R <= 16 || d.R <= 4 * d.E))
     return launch_linear_few(d, a, b, offsets, out, err, s);
   LinParams p;

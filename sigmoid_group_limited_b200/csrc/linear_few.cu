@@ -12,9 +12,11 @@
 // fp32, each lane over its pieces of K in order, then a butterfly over the
 // lanes: the same bits every time.
 //
-// Bound by HBM from some 32 rows on: 128 rows of 512 experts, 100 of them
-// touched, 768 x 2560 weights, 75 us = 5.3 TB/s; a token's 8 rows (31 MB) take
-// about 9 us, most of it launch, the offsets' latency and one round of loads.
+// Bound by HBM from some 64 rows on. Rows of as many experts, 768 x 2560 weights,
+// calls back to back in a graph, weights not in L2: 128 rows 83 us (6.1 TB/s), 64
+// rows 44 us (5.7), a token's 8 rows (31 MB) 9.5 us against 4.9 at the copy rate. There
+// the launch, the offsets' latency and 1.3 rounds of loads show (768 units on 592
+// blocks, a second unit's loads starting after the first one's sums).
 //
 // A unit is named by its first row: the blocks fill a table [R] with the
 // expert and the row count at every row that starts a unit, from one pass over
@@ -165,7 +167,10 @@ cudaError_t launch_linear_few(const moe_linear_desc& d, const void* x, const voi
                               const int32_t* offsets, void* y, int32_t* err, cudaStream_t s) {
   const FewParams p = {d.E, d.R, d.N, d.K, d.ld_x, d.ld_y, d.out_type == MOE_T_F32, d.accumulate != 0,
                        static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(W), offsets, y, err};
-  // short rows: more features per warp, so that as much is under way
+  // Short rows: more features per warp, so that as much is under way. A slab is 768,
+  // 1280 or 2560 long, and a row just above a length pays for all of the next: 64 rows
+  // of 768 features (timed as above) take 20 us with K = 1024, 23 with 1280, 35 with 1288, 36 with
+  // 1536, 39 with 2048, 44 with 2560, 63 with 2568 and 67 with 3840.
   if (d.K <= 768) return run<4, 3>(p, s);
   if (d.K <= 1280) return run<2, 5>(p, s);
   return run<1, 10>(p, s);

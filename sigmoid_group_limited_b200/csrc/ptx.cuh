@@ -16,8 +16,8 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // True in one lane of a converged warp. The compiler knows that a block under
 // it runs in a single lane and feeds TMA and tcgen05 instructions their
 // (uniform) operands directly; under `lane == 0` it wraps each one in a loop
-// over the active lanes, which costs a tcgen05.mma 215 cycles whatever its
-// size, against 173 (M = 256, N = 256), 109 (N = 128) and 81 (N = 64).
+// over the active lanes: a tcgen05.mma then takes 215 cycles whatever its size,
+// where one takes 128 by itself (M = 256, N = 256), 64 (N = 128) and 43 (N = 64).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
