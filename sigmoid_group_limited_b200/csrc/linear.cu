@@ -43,7 +43,7 @@
 //   reductions in L2 (subnormals flushed; one per element and pass, by the same
 //   thread in order, so the result is the same every time). A pass costs 6e-7 to
 //   7.5e-7 of the result's norm whatever the depth, and the P adds at most P 2^-24:
-//   7.4e-7 at a depth of 20011, 1.0e-6 at 1 M, 1.5e-6 at 4 M.
+//   7.4e-7 at a depth of 20011, 1.0e-6 at 1 M, 1.5e-6 at 4 M, 3.4e-6 at 2^25.
 //   bf16 results: passes of at most 16384, about 1e-4 of the sum or 1/40 of the
 //   final rounding; only wgrad is ever deeper. Their sum stays in tensor memory, in the
 //   accumulator that the passes leave free, and is rounded once.

@@ -1,13 +1,14 @@
 """The training operators at the ends of their ranges: gradient scales far
-from one, second moments below the normal numbers, gates far below zero, long contractions, waits that give up."""
+from one, second moments below the normal numbers, gates far below zero, long
+contractions, large weights, forked captures, waits that give up."""
 import time
 
 import pytest
 import torch
 
 import sigmoid_group_limited_b200 as sgl
-from tests.test_gpu_training import (BF, F8, F32, F64, HYPER, _adam_tensor, _check, _check_adam, _direct, _gen, _offsets,
-                                     _product, _randn, _run, _step)
+from tests.test_gpu_training import (BF, F8, F32, F64, HYPER, _adam_tensor, _check, _check_adam, _check_product, _direct,
+                                     _gen, _offsets, _product, _randn, _run, _step)
 
 pytestmark = pytest.mark.gpu
 
@@ -219,6 +220,66 @@ def test_fp32_results_do_not_lose_with_depth(direction, N, K, accumulate):
         errs.append(float((out.to(F64) - want).norm() / want.norm()))
     passes = -(-depths[1] // 768)
     assert errs[1] <= 2 * errs[0] + passes * 2.0 ** -24, errs
+
+
+# ------------------------------------------------------------------ addresses and graphs
+def test_weights_past_32_bits():
+    """More than 2^32 weights: experts on both sides of 2^31 and 2^32 elements, few and
+    many rows, and the clearing of experts without rows."""
+    gen = _gen(3)
+    E, N, K = 300, 4096, 4096
+    live = (0, 128, 256, 257, 299)
+    W = torch.zeros(E, N, K, dtype=BF, device="cuda")
+    for e in live:
+        W[e] = _randn((N, K), gen)
+    dW = torch.empty(E, N, K, dtype=BF, device="cuda")
+    for per in (8, 140):
+        counts = [per if e in live else 0 for e in range(E)]
+        off, R = _offsets(counts), per * len(live)
+        x, dy = _randn((R, K), gen), _randn((R, N), gen)
+        y, dx = torch.empty_like(dy), torch.empty_like(x)
+        for direction, a, out in (("linear", x, y), ("dgrad", dy, dx)):
+            ws = _run(direction, a, W, off, out)
+            ref, mag = _direct(direction, counts, a, W, out, False)
+            _check_product(out, ref, mag, 4096, torch.ones_like(out, dtype=torch.bool))
+        dW.fill_(3.0)
+        _run("wgrad", dy, x, off, dW, ws=ws)
+        assert sgl.moe_linear_read_error(ws) == 0
+        for e in range(E):
+            if e not in live:
+                assert not dW[e].any(), e
+        for i, e in enumerate(live):
+            want = dy[i * per:(i + 1) * per].to(F64).t() @ x[i * per:(i + 1) * per].to(F64)
+            mag = dy[i * per:(i + 1) * per].to(F64).abs().t() @ x[i * per:(i + 1) * per].to(F64).abs()
+            _check_product(dW[e], want, mag, per, torch.ones_like(dW[e], dtype=torch.bool))
+
+
+def test_captured_on_two_streams_that_join():
+    """A capture that forks after a fill and joins before the next operator: the
+    operators' launches have several predecessors, some of them no kernels."""
+    x, W, _ = _product("linear", [100, 200], 72, 136, seed=19)
+    off = _offsets([100, 200])
+    y = [torch.empty(300, 72, dtype=BF, device="cuda") for _ in range(3)]
+    h, want = torch.empty_like(y[0]), torch.empty_like(y[0])
+    ws = _run("linear", x, W, off, y[2])
+    sgl.moe_swiglu(y[2], y[2], want)
+    torch.cuda.synchronize()
+    side, gr = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        main = torch.cuda.current_stream()
+        y[0].zero_()
+        side.wait_stream(main)
+        _run("linear", x, W, off, y[0], ws=ws)
+        with torch.cuda.stream(side):
+            y[1].zero_()
+            _run("linear", x, W, off, y[1], ws=ws)
+        main.wait_stream(side)
+        sgl.moe_swiglu(y[0], y[1], h)
+    for _ in range(3):
+        h.zero_()
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y[0], y[2]) and torch.equal(y[1], y[2]) and torch.equal(h, want)
 
 
 # ------------------------------------------------------------------ waits that give up
